@@ -11,6 +11,7 @@ this package without libbq.so raises, and there is no CPU fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -26,6 +27,7 @@ DT = {"bf16": 0, "fp16": 1, "fp32": 2, "ue8m0": 3, "e4m3": 4}
 FORMATS = {"int8_sym": 0, "int8_asym": 1, "int4_sym": 2, "uint4_asym": 3, "e4m3": 4, "e5m2": 5, "e2m1": 6,
            "e2m3": 7, "e3m2": 8}
 GRANULARITIES = {"tensor": 0, "row": 1, "group": 2, "mx": 3, "nv": 4, "tile2d": 5}
+ACTS = {"silu": 0, "gelu": 1}          # gated activations ("gelu": its tanh form)
 LAYOUTS = {"rows": 0, "gemm": 1}       # MX / NV block scales: row-major, or a block-scaled GEMM's tiles
 FOUR_BIT = {"int4_sym", "uint4_asym", "e2m1"}
 ASYMMETRIC = {"int8_asym", "uint4_asym"}
@@ -94,6 +96,15 @@ def _lib() -> ctypes.CDLL:
         L.bq_quantize_batch.argtypes = [vp, i32, i64, i64, i64, sp, vp, vp, vp, vp, vp, sz, vp]
         L.bq_gemm.restype = ctypes.c_int
         L.bq_gemm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, sp, vp, i32, vp]
+        for f in (L.bq_linear, L.bq_linear_grad_input):
+            f.restype = ctypes.c_int
+            f.argtypes = [vp, i32, i64, vp, vp, vp, i64, i64, i64, sp, vp, i32, vp]
+        L.bq_linear_grad_weight.restype = ctypes.c_int
+        L.bq_linear_grad_weight.argtypes = [vp, i32, i64, vp, vp, i64, i64, i64, sp, vp, i32, vp]
+        L.bq_glu.restype = ctypes.c_int
+        L.bq_glu.argtypes = [vp, i64, vp, i64, i32, i64, i64, i32, vp, sp, vp, vp, vp, vp, vp]
+        L.bq_glu_backward.restype = ctypes.c_int
+        L.bq_glu_backward.argtypes = [vp, i64, i32, vp, vp, vp, vp, sp, i64, i64, i32, vp, i64, vp, i64, vp]
         L.bq_debug_skip_tile_copy.restype = ctypes.c_int
         L.bq_debug_skip_tile_copy.argtypes = [i32]
         L.bq_wait_timeouts.restype = ctypes.c_int
@@ -502,3 +513,208 @@ def qsnr(x: torch.Tensor, q: Quantized, workspace: torch.Tensor | None = None, s
         workspace = new_workspace(x.device)
     bq_qsnr(x.contiguous(), q.codes, q.scales, q.zero_points, q.tensor_scale, q.scheme, st, workspace, stream)
     return st
+
+
+# ---------------------------------------------------------------------------
+# A linear layer over block-scaled data, and the gated activation between two of them
+# ---------------------------------------------------------------------------
+
+_OUT_DT = {torch.bfloat16: 0, torch.float32: 2}
+
+
+def _c_scheme(scheme: Scheme) -> BqScheme:
+    """scheme.c(), kept on the scheme (a frozen value), for the calls whose host time counts."""
+    c = scheme.__dict__.get("_c")
+    if c is None:
+        c = scheme.c()
+        object.__setattr__(scheme, "_c", c)
+    return c
+
+
+def _elsewhere(dev: torch.device, stream) -> bool:
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _on(dev: torch.device, stream):
+    """dev, and the given stream if any, current: whatever a call allocates, copies and launches
+    goes there."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the codes on {dev}")
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _check_operand(t: torch.Tensor, name: str, cols: int, dev: torch.device) -> None:
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D bf16 CUDA tensor")
+    if t.shape[1] != cols:
+        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the codes on {dev}")
+
+
+def _ld(t: torch.Tensor, step: int) -> int:
+    """Elements between t's rows (a tensor of at most one row, or of none to a row, has no
+    such distance: any valid value)."""
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] else -(-t.shape[1] // step) * step
+
+
+def _rows_apart(t: torch.Tensor, step: int) -> torch.Tensor:
+    """t, or a copy of it, with unit column stride, rows a multiple of step elements apart
+    and the first element 2 * step bytes aligned."""
+    rows, cols = t.shape
+    ld = _ld(t, step)
+    if (t.stride(1) == 1 or cols == 1) and ld >= cols and ld % step == 0 and t.data_ptr() % (2 * step) == 0:
+        return t
+    buf = torch.empty((rows, -(-cols // step) * step), dtype=t.dtype, device=t.device)[:, :cols]
+    buf.copy_(t)
+    return buf
+
+
+def _out(out: torch.Tensor | None, rows: int, cols: int, dtype, dev: torch.device) -> torch.Tensor:
+    if dtype not in _OUT_DT:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=dev)
+    if out.shape != (rows, cols) or out.dtype not in _OUT_DT or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous bf16 or fp32 [{rows}, {cols}] tensor on {dev}")
+    return out
+
+
+def linear(x: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+           stream=None) -> torch.Tensor:
+    """x W^T: bf16 x [m, k] (rows may be apart) and a 4-bit weight w (E2M1 under "mx" or "nv")
+    of [n, k] -> [m, n] of dtype (or of out's)."""
+    dev = w.codes.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return linear(x, w, dtype, out)
+    _check_operand(x, "x", w.cols, dev)
+    x = _rows_apart(x, 8)
+    m = x.shape[0]
+    y = _out(out, m, w.rows, dtype, dev)
+    _check(_lib().bq_linear(x.data_ptr(), 0, _ld(x, 8), w.codes.data_ptr(), w.scales.data_ptr(),
+                            _ptr(w.tensor_scale), m, w.rows, w.cols, ctypes.byref(_c_scheme(w.scheme)), y.data_ptr(),
+                            _OUT_DT[y.dtype], _stream(None)), "bq_linear")
+    return y
+
+
+def linear_grad_input(dy: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """dy W: the gradient of linear's x, from bf16 dy [m, n] and the weight [n, k] -> [m, k]."""
+    dev = w.codes.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return linear_grad_input(dy, w, dtype, out)
+    _check_operand(dy, "dy", w.rows, dev)
+    dy = _rows_apart(dy, 8)
+    m = dy.shape[0]
+    dx = _out(out, m, w.cols, dtype, dev)
+    _check(_lib().bq_linear_grad_input(dy.data_ptr(), 0, _ld(dy, 8), w.codes.data_ptr(), w.scales.data_ptr(),
+                                       _ptr(w.tensor_scale), m, w.rows, w.cols, ctypes.byref(_c_scheme(w.scheme)),
+                                       dx.data_ptr(), _OUT_DT[dx.dtype], _stream(None)), "bq_linear_grad_input")
+    return dx
+
+
+def linear_grad_weight(dy: torch.Tensor, x: Quantized, dtype=torch.float32, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """dy^T X: the gradient of linear's weight, from bf16 dy [m, n] and the layer's input kept
+    in 8 bits (E4M3, E5M2 or INT8 under "mx") x of [m, k] -> [n, k]."""
+    dev = x.codes.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return linear_grad_weight(dy, x, dtype, out)
+    if dy.dim() != 2 or dy.shape[0] != x.rows:
+        raise ValueError(f"dy must be [{x.rows}, n], as many rows as the kept input")
+    n = dy.shape[1]
+    _check_operand(dy, "dy", n, dev)
+    dy = _rows_apart(dy, 8)
+    dw = _out(out, n, x.cols, dtype, dev)
+    _check(_lib().bq_linear_grad_weight(dy.data_ptr(), 0, _ld(dy, 8), x.codes.data_ptr(), x.scales.data_ptr(), x.rows,
+                                        n, x.cols, ctypes.byref(_c_scheme(x.scheme)), dw.data_ptr(), _OUT_DT[dw.dtype],
+                                        _stream(None)), "bq_linear_grad_weight")
+    return dw
+
+
+@dataclass
+class GluCheckpoint:
+    """What glu keeps for glu_backward: the gate and the up projection in 8 bits."""
+    gate: Quantized
+    up: Quantized
+    act: str
+
+
+def glu(gate: torch.Tensor, up: torch.Tensor, scheme: Scheme | None = None, act: str = "silu",
+        out: torch.Tensor | None = None, ckpt: GluCheckpoint | None = None, stream=None):
+    """h = a(gate) up of bf16 [rows, cols] tensors (rows may be apart, e.g. the halves of one
+    [rows, 2 cols] tensor) -> (h, GluCheckpoint), the copies quantized under scheme (E4M3,
+    E5M2 or INT8 with "mx"; to ckpt's buffers when given); without a scheme (h, None)."""
+    if gate.dim() != 2 or gate.shape != up.shape:
+        raise ValueError("gate and up must be 2-D tensors of the same shape")
+    rows, cols = gate.shape
+    dev = gate.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return glu(gate, up, scheme, act, out, ckpt)
+    _check_operand(gate, "gate", cols, dev)
+    _check_operand(up, "up", cols, dev)
+    gate, up = _rows_apart(gate, 16), _rows_apart(up, 16)
+    h = _out(out, rows, cols, torch.bfloat16, dev)
+    if h.dtype != torch.bfloat16:
+        raise ValueError("out must be bf16")
+    if scheme is None:
+        if ckpt is not None:
+            raise ValueError("a checkpoint needs a scheme")
+        _check(_lib().bq_glu(gate.data_ptr(), _ld(gate, 16), up.data_ptr(), _ld(up, 16), 0, rows, cols, ACTS[act],
+                             h.data_ptr(), None, None, None, None, None, _stream(None)), "bq_glu")
+        return h, None
+    if ckpt is None:
+        ckpt = GluCheckpoint(alloc_outputs(scheme, rows, cols, dev, False),
+                             alloc_outputs(scheme, rows, cols, dev, False), act)
+    s, g, u = scheme.resolved(), ckpt.gate, ckpt.up
+    if g.scheme != s or u.scheme != s or (g.rows, g.cols) != (rows, cols) or (u.rows, u.cols) != (rows, cols):
+        raise ValueError("the checkpoint's buffers are of another scheme or shape")
+    if g.codes.device != dev or u.codes.device != dev:
+        raise ValueError(f"the checkpoint's buffers are not on {dev}")
+    ckpt.act = act
+    _check(_lib().bq_glu(gate.data_ptr(), _ld(gate, 16), up.data_ptr(), _ld(up, 16), 0, rows, cols, ACTS[act],
+                         h.data_ptr(), ctypes.byref(_c_scheme(s)), g.codes.data_ptr(), g.scales.data_ptr(),
+                         u.codes.data_ptr(), u.scales.data_ptr(), _stream(None)), "bq_glu")
+    return h, ckpt
+
+
+def glu_backward(dh: torch.Tensor, ckpt: GluCheckpoint, out=None, stream=None):
+    """(dgate, dup) of glu from bf16 dh [rows, cols] and what glu kept; out: two bf16 tensors
+    to write (unit column stride, rows a multiple of 16 elements apart, e.g. the halves of
+    one [rows, 2 cols] tensor)."""
+    g, u = ckpt.gate, ckpt.up
+    dev, rows, cols = g.codes.device, g.rows, g.cols
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return glu_backward(dh, ckpt, out)
+    if dh.dim() != 2 or dh.shape[0] != rows or (u.rows, u.cols, u.scheme) != (rows, cols, g.scheme):
+        raise ValueError("dh and the two copies must be of one shape")
+    _check_operand(dh, "dh", cols, dev)
+    dh = _rows_apart(dh, 16)
+    if out is None:
+        out = (torch.empty((rows, cols), dtype=torch.bfloat16, device=dev),
+               torch.empty((rows, cols), dtype=torch.bfloat16, device=dev))
+    dg, du = out
+    for t in (dg, du):
+        _check_operand(t, "out", cols, dev)
+        if t.shape[0] != rows or (t.stride(1) != 1 and cols > 1):
+            raise ValueError(f"out must be [{rows}, {cols}] tensors with unit column stride")
+    _check(_lib().bq_glu_backward(dh.data_ptr(), _ld(dh, 16), 0, g.codes.data_ptr(), g.scales.data_ptr(),
+                                  u.codes.data_ptr(), u.scales.data_ptr(), ctypes.byref(_c_scheme(g.scheme)), rows,
+                                  cols, ACTS[ckpt.act], dg.data_ptr(), _ld(dg, 16), du.data_ptr(), _ld(du, 16),
+                                  _stream(None)), "bq_glu_backward")
+    return dg, du

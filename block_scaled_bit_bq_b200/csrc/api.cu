@@ -605,10 +605,11 @@ bq_status bq_dequantize_rt(const void* codes, const void* scales, const void* ze
 bq_status bq_wait_timeouts(uint32_t* count, int32_t reset)
 {
     if (!count) return BQ_ERR_INVALID_ARG;
-    unsigned int c = 0, g = 0;
+    unsigned int c = 0, g = 0, l = 0;
     if (bq::flat_wait_timeouts(&c, reset != 0) != cudaSuccess) return BQ_ERR_CUDA;
     if (bq::gemm_wait_timeouts(&g, reset != 0) != cudaSuccess) return BQ_ERR_CUDA;
-    *count = c + g;
+    if (bq::linear_wait_timeouts(&l, reset != 0) != cudaSuccess) return BQ_ERR_CUDA;
+    *count = c + g + l;
     return BQ_OK;
 }
 
@@ -659,6 +660,159 @@ bq_status bq_gemm(const void* a_codes, const void* a_scales, const float* a_tens
     g.elem_fmt = fmt_code;
     g.d_bf16 = d_dtype == BQ_DT_BF16 ? 1 : 0;
     return cuda_status(launch_gemm(kind, g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15u) == 0; }
+
+size_t out_size(int32_t dtype) { return dtype == BQ_DT_BF16 ? 2 : 4; }
+
+bool mx8(const Plan& p)
+{
+    return p.gran == BQ_MX_BLOCK && (p.fmt == BQ_FP8_E4M3 || p.fmt == BQ_FP8_E5M2 || p.fmt == BQ_INT8_SYM) && !p.had;
+}
+
+// The three products of a linear layer: x is the bf16 operand [m, x_cols], the codes are
+// [q_rows, k], out is [nj, ni], summed over nc.
+bq_status linear_call(int op, const void* x, int32_t x_dtype, int64_t ldx, const void* codes, const void* scales,
+                      const float* tensor_scale, int64_t m, int64_t n, int64_t k, const bq_scheme* scheme, void* out,
+                      int32_t out_dtype, void* stream)
+{
+    const int64_t q_rows = op == LIN_GRAD_WEIGHT ? m : n;
+    Plan p;
+    const bq_status st = make_plan(scheme, q_rows, k, &p);
+    if (st != BQ_OK) return st;
+    if (op == LIN_GRAD_WEIGHT ? !mx8(p) : (p.fmt != BQ_FP4_E2M1 || p.had)) return BQ_ERR_UNSUPPORTED;
+    if (x_dtype != BQ_DT_BF16 || (out_dtype != BQ_DT_BF16 && out_dtype != BQ_DT_FP32)) return BQ_ERR_UNSUPPORTED;
+    const int64_t x_cols = op == LIN_FORWARD ? k : n;
+    const int64_t nj = op == LIN_GRAD_WEIGHT ? n : m, ni = op == LIN_FORWARD ? n : k;
+    const int64_t nc = op == LIN_FORWARD ? k : (op == LIN_GRAD_INPUT ? n : m);
+    if (m < 0 || n < 0 || m >= (1ll << 31) || n >= (1ll << 31) || k % 32 != 0) return BQ_ERR_SHAPE;
+    if (ldx < x_cols || ldx % 8 != 0 || ldx >= (1ll << 31)) return BQ_ERR_SHAPE;
+    if ((uint64_t)nj * (uint64_t)ni > MAX_ELEMS || (uint64_t)m * (uint64_t)x_cols > MAX_ELEMS) return BQ_ERR_SHAPE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (nj == 0 || ni == 0) return BQ_OK;
+    if (!out) return BQ_ERR_INVALID_ARG;
+    if (!aligned16(out)) return BQ_ERR_ALIGNMENT;
+    if (nc == 0) return cuda_status(cudaMemsetAsync(out, 0, (size_t)nj * (size_t)ni * out_size(out_dtype), s));
+    if (!x || !codes || !scales) return BQ_ERR_INVALID_ARG;
+    if (p.gran == BQ_NV_BLOCK && !tensor_scale) return BQ_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned32(codes) || !aligned4(scales) || !aligned4(tensor_scale)) return BQ_ERR_ALIGNMENT;
+    LinearArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.x = x; a.codes = reinterpret_cast<const uint8_t*>(codes); a.scales = reinterpret_cast<const uint8_t*>(scales);
+    a.tensor_scale = p.gran == BQ_NV_BLOCK ? tensor_scale : nullptr;
+    a.out = out; a.ldx = (uint64_t)ldx;
+    a.x_rows = (uint32_t)m; a.x_cols = (uint32_t)x_cols;
+    a.q_rows = (uint32_t)q_rows; a.k = (uint32_t)k; a.nb = p.nb;
+    a.nj = (uint32_t)nj; a.ni = (uint32_t)ni; a.nc = (uint32_t)nc;
+    a.gemm_layout = p.gemm_layout ? 1 : 0;
+    a.out_bf16 = out_dtype == BQ_DT_BF16 ? 1 : 0;
+    return cuda_status(launch_linear(op, p.fmt, p.gran == BQ_NV_BLOCK, a, s));
+}
+
+// Checks shared by the gated activation's two passes: an 8-bit MX scheme with row-major scales.
+bq_status glu_check(const bq_scheme* scheme, int64_t rows, int64_t cols, Plan* p)
+{
+    const bq_status st = make_plan(scheme, rows, cols, p);
+    if (st != BQ_OK) return st;
+    return mx8(*p) && !p->gemm_layout ? BQ_OK : BQ_ERR_UNSUPPORTED;
+}
+
+bool glu_ld(int64_t ld, int64_t cols) { return ld >= cols && ld % 16 == 0 && ld < (1ll << 31); }
+
+}  // namespace
+
+bq_status bq_linear(const void* x, int32_t x_dtype, int64_t ldx, const void* w_codes, const void* w_scales,
+                    const float* w_tensor_scale, int64_t m, int64_t n, int64_t k, const bq_scheme* scheme, void* y,
+                    int32_t out_dtype, void* stream)
+{
+    return linear_call(LIN_FORWARD, x, x_dtype, ldx, w_codes, w_scales, w_tensor_scale, m, n, k, scheme, y, out_dtype,
+                       stream);
+}
+
+bq_status bq_linear_grad_input(const void* dy, int32_t dy_dtype, int64_t lddy, const void* w_codes,
+                               const void* w_scales, const float* w_tensor_scale, int64_t m, int64_t n, int64_t k,
+                               const bq_scheme* scheme, void* dx, int32_t out_dtype, void* stream)
+{
+    return linear_call(LIN_GRAD_INPUT, dy, dy_dtype, lddy, w_codes, w_scales, w_tensor_scale, m, n, k, scheme, dx,
+                       out_dtype, stream);
+}
+
+bq_status bq_linear_grad_weight(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x_codes,
+                                const void* x_scales, int64_t m, int64_t n, int64_t k, const bq_scheme* scheme,
+                                void* dw, int32_t out_dtype, void* stream)
+{
+    return linear_call(LIN_GRAD_WEIGHT, dy, dy_dtype, lddy, x_codes, x_scales, nullptr, m, n, k, scheme, dw, out_dtype,
+                       stream);
+}
+
+bq_status bq_glu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype, int64_t rows,
+                 int64_t cols, int32_t act, void* out, const bq_scheme* scheme, void* gate_codes, void* gate_scales,
+                 void* up_codes, void* up_scales, void* stream)
+{
+    Plan p;
+    int fmt = -1;
+    if (scheme) {
+        const bq_status st = glu_check(scheme, rows, cols, &p);
+        if (st != BQ_OK) return st;
+        fmt = p.fmt;
+    } else {
+        // the shape rules of the 8-bit copies, so that a call does not depend on their presence
+        const bq_scheme any{BQ_FP8_E4M3, BQ_MX_BLOCK, 32, BQ_DT_UE8M0, 0, BQ_LAYOUT_ROWS};
+        const bq_status st = glu_check(&any, rows, cols, &p);
+        if (st != BQ_OK) return st;
+        if (gate_codes || gate_scales || up_codes || up_scales) return BQ_ERR_INVALID_ARG;
+    }
+    if (act != BQ_ACT_SILU && act != BQ_ACT_GELU_TANH) return BQ_ERR_INVALID_ARG;
+    if (dtype != BQ_DT_BF16) return BQ_ERR_UNSUPPORTED;
+    if (!glu_ld(ld_gate, cols) || !glu_ld(ld_up, cols)) return BQ_ERR_SHAPE;
+    if (p.n == 0) return BQ_OK;
+    if (!gate || !up || !out) return BQ_ERR_INVALID_ARG;
+    if (scheme && (!gate_codes || !gate_scales || !up_codes || !up_scales)) return BQ_ERR_INVALID_ARG;
+    if (!aligned32(gate) || !aligned32(up) || !aligned32(out) || !aligned32(gate_codes) || !aligned32(up_codes))
+        return BQ_ERR_ALIGNMENT;
+    if (!aligned4(gate_scales) || !aligned4(up_scales)) return BQ_ERR_ALIGNMENT;
+    GluArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.x0 = gate; a.x1 = up; a.y0 = out;
+    a.codes0 = reinterpret_cast<uint8_t*>(gate_codes); a.codes1 = reinterpret_cast<uint8_t*>(up_codes);
+    a.scales0 = reinterpret_cast<uint8_t*>(gate_scales); a.scales1 = reinterpret_cast<uint8_t*>(up_scales);
+    a.ldx0 = (uint64_t)ld_gate; a.ldx1 = (uint64_t)ld_up; a.ldy0 = (uint64_t)cols;
+    a.n_chunks = p.n_chunks;
+    a.cpr = make_fastdiv((uint32_t)(cols / 16));
+    return cuda_status(launch_glu(fmt, act, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bq_status bq_glu_backward(const void* dh, int64_t ld_dh, int32_t dtype, const void* gate_codes,
+                          const void* gate_scales, const void* up_codes, const void* up_scales,
+                          const bq_scheme* scheme, int64_t rows, int64_t cols, int32_t act, void* dgate,
+                          int64_t ld_dgate, void* dup, int64_t ld_dup, void* stream)
+{
+    Plan p;
+    const bq_status st = glu_check(scheme, rows, cols, &p);
+    if (st != BQ_OK) return st;
+    if (act != BQ_ACT_SILU && act != BQ_ACT_GELU_TANH) return BQ_ERR_INVALID_ARG;
+    if (dtype != BQ_DT_BF16) return BQ_ERR_UNSUPPORTED;
+    if (!glu_ld(ld_dh, cols) || !glu_ld(ld_dgate, cols) || !glu_ld(ld_dup, cols)) return BQ_ERR_SHAPE;
+    if (p.n == 0) return BQ_OK;
+    if (!dh || !gate_codes || !gate_scales || !up_codes || !up_scales || !dgate || !dup) return BQ_ERR_INVALID_ARG;
+    if (dgate == dup) return BQ_ERR_INVALID_ARG;
+    if (!aligned32(dh) || !aligned32(gate_codes) || !aligned32(up_codes) || !aligned32(dgate) || !aligned32(dup))
+        return BQ_ERR_ALIGNMENT;
+    if (!aligned4(gate_scales) || !aligned4(up_scales)) return BQ_ERR_ALIGNMENT;
+    GluArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.x0 = dh; a.y0 = dgate; a.y1 = dup;
+    a.codes0 = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(gate_codes));
+    a.codes1 = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(up_codes));
+    a.scales0 = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(gate_scales));
+    a.scales1 = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(up_scales));
+    a.ldx0 = (uint64_t)ld_dh; a.ldy0 = (uint64_t)ld_dgate; a.ldy1 = (uint64_t)ld_dup;
+    a.n_chunks = p.n_chunks;
+    a.cpr = make_fastdiv((uint32_t)(cols / 16));
+    return cuda_status(launch_glu_backward(p.fmt, act, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 double bq_stats_qsnr_db(const bq_stats* host_stats)

@@ -150,6 +150,51 @@ cudaError_t launch_gemm(int kind, const GemmArgs& g, cudaStream_t st);
 // Waits of the GEMM kernel that gave up (each leaves that call's D incomplete). Synchronous.
 cudaError_t gemm_wait_timeouts(unsigned int* count, bool reset);
 
+// The products of a linear layer over block-scaled data (linear.cu): out[j, i] = sum_c X(j, c)
+// Q(i, c) with X bf16 and Q block-scaled codes.
+//   LIN_FORWARD:     j = token, i = weight row n,  c = k: X = x [m, k],  Q = W [n, k]
+//   LIN_GRAD_INPUT:  j = token, i = column k,      c = n: X = dy [m, n], Q = W [n, k]
+//   LIN_GRAD_WEIGHT: j = n,     i = column k,      c = token: X = dy [m, n], Q = X8 [m, k]
+enum { LIN_FORWARD = 0, LIN_GRAD_INPUT = 1, LIN_GRAD_WEIGHT = 2 };
+
+struct LinearArgs {
+    const void* x;              // bf16 rows, ldx elements apart
+    const uint8_t* codes;       // [q_rows, k] (FP4: k / 2 bytes a row)
+    const uint8_t* scales;
+    const float* tensor_scale;  // NV, else null
+    void* out;                  // [nj, ni] contiguous
+    uint64_t ldx;
+    uint32_t x_rows, x_cols;    // of x as stored: (m, k) or (m, n)
+    uint32_t q_rows, k;         // of the codes
+    uint32_t nb;                // scale blocks per row
+    uint32_t nj, ni, nc;        // output rows, output columns, contraction length
+    int32_t gemm_layout;
+    int32_t out_bf16;
+};
+
+cudaError_t launch_linear(int op, int fmt, bool nv, const LinearArgs& a, cudaStream_t st);
+// Waits of the linear kernels that gave up (each leaves that call's output incomplete). Synchronous.
+cudaError_t linear_wait_timeouts(unsigned int* count, bool reset);
+
+// The gated activation (glu.cu). Forward: x0 = gate, x1 = up, y0 = h, codes and scales written
+// (null: none). Backward: x0 = dh, codes and scales read, y0 = dgate, y1 = dup.
+struct GluArgs {
+    const void* x0;
+    const void* x1;
+    uint8_t* codes0;
+    uint8_t* codes1;
+    uint8_t* scales0;
+    uint8_t* scales1;
+    void* y0;
+    void* y1;
+    uint64_t ldx0, ldx1, ldy0, ldy1;   // elements
+    uint32_t n_chunks;                 // rows * cols / 16
+    FastDiv cpr;                       // division by chunks per row
+};
+
+cudaError_t launch_glu(int fmt, int act, const GluArgs& a, cudaStream_t st);           // fmt -1: no copies
+cudaError_t launch_glu_backward(int fmt, int act, const GluArgs& a, cudaStream_t st);
+
 // Scale kinds for dequantize / QSNR.
 enum { SK_F32 = 0, SK_F16 = 1, SK_UE8M0 = 2, SK_NV = 3 };
 

@@ -368,6 +368,92 @@ bq_status bq_gemm(const void* a_codes, const void* a_scales, const float* a_tens
                   void* d, int32_t d_dtype, void* stream);
 
 /*
+ * A linear layer over block-scaled data: the product of unquantized bf16 activations with
+ * a 4-bit weight, and its two gradients. ("Quantization survey" §4.3: MXFP4 and NVFP4 hold
+ * a weight in about 4.25 and 4.5 bits a value; its FP8-training recipe keeps activations in
+ * 8 bits for the backward pass. The pages give no weight-only product: this is the form in
+ * which a weight quantized once serves activations of any number of tokens.)
+ *
+ *   bq_linear:              y[t, n]  = sum_k x[t, k]  W[n, k]
+ *   bq_linear_grad_input:   dx[t, k] = sum_n dy[t, n] W[n, k]
+ *   bq_linear_grad_weight:  dw[n, k] = sum_t dy[t, n] X[t, k]
+ *
+ * W [n, k] is a BQ_FP4_E2M1 weight under BQ_MX_BLOCK or BQ_NV_BLOCK, X [m, k] the layer's
+ * input kept in 8 bits (BQ_FP8_E4M3, BQ_FP8_E5M2 or BQ_INT8_SYM under BQ_MX_BLOCK): codes
+ * and scales as bq_quantize wrote them for [n, k] (for [m, k]), in either scale layout,
+ * tensor_scale the NV tensor scale (device, one fp32; NULL under MX). hadamard = 0. Other
+ * schemes: BQ_ERR_UNSUPPORTED.
+ *
+ * Values: a code times its block's scale is a bf16 value (below 2^-126 only when an MX block's
+ * largest magnitude is under 2^-117; such values are rounded to a multiple of 2^-133), so every
+ * product of a value and an activation is exact in fp32; sums are fp32 (on the tensor cores, in
+ * their order; not bit-exact with any CPU order), NV's tensor scale multiplies the finished sum,
+ * and the result is rounded once to the output type (fp32, or bf16 round to nearest even). A
+ * call gives the same bits every time for the same inputs and sizes.
+ *
+ * x [m, k], dy [m, n]: bf16 (x_dtype / dy_dtype = BQ_DT_BF16), rows of ld elements apart
+ * (ld >= the row's length, ld % 8 == 0), 16-byte aligned. Outputs y [m, n], dx [m, k] and
+ * dw [n, k] are contiguous and 16-byte aligned, of type out_dtype (BQ_DT_FP32 or
+ * BQ_DT_BF16), and may not overlap the inputs. Any m >= 0 and n >= 0; k > 0, k % 32 == 0
+ * (else BQ_ERR_SHAPE); m, n, k, ld < 2^31, m * k, m * n and n * k at most 2^36 - 2048.
+ * m == 0 (n == 0): an output without elements is left alone, and a gradient that sums over
+ * no tokens (no outputs) is set to zero. Codes: 32-byte aligned; scales and the tensor scale
+ * 4-byte aligned (BQ_ERR_ALIGNMENT). Non-finite x or dy follow IEEE arithmetic. No workspace;
+ * enqueued on stream; every wait in the kernels is bounded (bq_wait_timeouts counts those that
+ * gave up).
+ */
+bq_status bq_linear(const void* x, int32_t x_dtype, int64_t ldx,
+                    const void* w_codes, const void* w_scales, const float* w_tensor_scale,
+                    int64_t m, int64_t n, int64_t k, const bq_scheme* scheme,
+                    void* y, int32_t out_dtype, void* stream);
+
+bq_status bq_linear_grad_input(const void* dy, int32_t dy_dtype, int64_t lddy,
+                               const void* w_codes, const void* w_scales, const float* w_tensor_scale,
+                               int64_t m, int64_t n, int64_t k, const bq_scheme* scheme,
+                               void* dx, int32_t out_dtype, void* stream);
+
+bq_status bq_linear_grad_weight(const void* dy, int32_t dy_dtype, int64_t lddy,
+                                const void* x_codes, const void* x_scales,
+                                int64_t m, int64_t n, int64_t k, const bq_scheme* scheme,
+                                void* dw, int32_t out_dtype, void* stream);
+
+/*
+ * The gated activation between two linear layers, with the 8-bit copies that its backward
+ * pass needs, and that backward pass.
+ *
+ *   bq_glu:           h = a(g) u;  G, U = g, u quantized (codes and scales exactly those of
+ *                     bq_quantize under scheme)
+ *   bq_glu_backward:  du = dh a(G),  dg = dh U a'(G)   (G, U the dequantized copies)
+ *
+ * a(g) = g s(v), s the logistic function: v = g for BQ_ACT_SILU, v = 2 sqrt(2 / pi)
+ * (g + 0.044715 g^3) for BQ_ACT_GELU_TANH (the tanh form of GELU). Arithmetic in fp32
+ * (exp2 and reciprocal approximations of about 2^-22 relative error), each result rounded
+ * once to bf16. The forward pass uses g and u as given, not their copies.
+ *
+ * scheme: BQ_MX_BLOCK with BQ_FP8_E4M3, BQ_FP8_E5M2 or BQ_INT8_SYM, BQ_LAYOUT_ROWS,
+ * hadamard = 0 (else BQ_ERR_UNSUPPORTED). bq_glu with scheme == NULL computes h alone (for
+ * inference; the four copy buffers must then be NULL, else BQ_ERR_INVALID_ARG).
+ * gate, up, dh, dgate, dup: bf16 [rows, cols], rows of their own ld elements apart
+ * (ld >= cols, ld % 16 == 0: e.g. the two halves of one [rows, 2 cols] tensor), 32-byte
+ * aligned; out: bf16 [rows, cols] contiguous, 32-byte aligned; codes uint8 [rows, cols],
+ * 32-byte aligned; scales uint8 [rows, cols / 32], 4-byte aligned. cols % 32 == 0;
+ * rows >= 0 (0: nothing is done); rows * cols <= 2^36 - 2048. Outputs may not overlap the
+ * inputs or each other (dgate == dup: BQ_ERR_INVALID_ARG). NaN or Inf in g or u give
+ * unspecified results in their own 32-element block. No workspace; enqueued on stream.
+ */
+enum { BQ_ACT_SILU = 0, BQ_ACT_GELU_TANH = 1 };
+
+bq_status bq_glu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype,
+                 int64_t rows, int64_t cols, int32_t act, void* out, const bq_scheme* scheme,
+                 void* gate_codes, void* gate_scales, void* up_codes, void* up_scales, void* stream);
+
+bq_status bq_glu_backward(const void* dh, int64_t ld_dh, int32_t dtype,
+                          const void* gate_codes, const void* gate_scales,
+                          const void* up_codes, const void* up_scales, const bq_scheme* scheme,
+                          int64_t rows, int64_t cols, int32_t act,
+                          void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup, void* stream);
+
+/*
  * Bounded waits. The quantize kernels stage their input tiles in shared memory with
  * tensor-map bulk copies and wait for each on an mbarrier; a wait that has not
  * completed after about one second gives up instead of hanging. The kernel then stops
