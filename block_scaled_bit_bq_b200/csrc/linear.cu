@@ -1,105 +1,593 @@
 // linear.cu -- the products of a linear layer over block-scaled data (bq_linear and its two
-// gradients): out[j, i] = sum_c X(j, c) Q(i, c), X bf16, Q block-scaled codes, each role of
+// gradients): out[j, i] = sum_c X(j, c) Q(i, c), X bf16, Q block-scaled codes, the roles of
 // the stored matrices as LinearArgs says.
+//
+// Every code times its block scale is a bf16 value (widen.cuh), so the codes are widened to
+// bf16 on the way to the tensor cores and the products with X are exact; sums are fp32.
+//
+// Two kernels:
+//  - k_linear_mma, on the fifth-generation tensor cores: out's transpose in tiles of 128
+//    (i, from Q) x up to 256 (j, from X);
+//  - k_linear_rows, for the forward product of a few tokens, where the weight's bytes are all
+//    that counts: the codes go straight from global memory to mma.sync fragments.
 #include "internal.h"
+#include "tc.cuh"
+#include "widen.cuh"
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
 
 namespace bq {
 
+__device__ unsigned int g_linear_wait_timeouts = 0;
+
 namespace {
 
-// One code's value times its block's scale (without NV's tensor scale).
-template <int FMT, bool NV>
-__device__ __forceinline__ float code_value(const LinearArgs& a, uint32_t row, uint32_t col)
+// ---------------------------------------------------------------------------
+// Shared pieces
+// ---------------------------------------------------------------------------
+
+// Byte offset of block scale (row, blk) in either scale layout. Scales of an even block and
+// the one after it are adjacent in both.
+__device__ __forceinline__ size_t scale_offset(const LinearArgs& a, uint32_t row, uint32_t blk)
 {
-    float v;
-    if constexpr (FMT == BQ_FP4_E2M1) {
-        const uint32_t b = a.codes[(size_t)row * (a.k / 2) + col / 2];
-        v = dec_pair<FMT>((b >> (4 * (col & 1))) & 0xFu).x;
-    } else {
-        const uint32_t b = a.codes[(size_t)row * a.k + col];
-        v = FMT == BQ_INT8_SYM ? (float)(int8_t)b : dec_pair<FMT == BQ_INT8_SYM ? BQ_FP8_E4M3 : FMT>(b).x;
-    }
-    const uint32_t blk = col / (NV ? 16u : 32u);
-    const size_t so = a.gemm_layout ? gemm_scale_offset(row, blk, a.nb) : (size_t)row * a.nb + blk;
-    const uint32_t sc = a.scales[so];
-    return __fmul_rn(v, NV ? e4m3_value(sc) : exp2i((int)sc - 127));
+    return a.gemm_layout ? (size_t)gemm_scale_offset(row, blk, a.nb) : (size_t)row * a.nb + blk;
 }
 
-constexpr int T = 32;
+__device__ __forceinline__ uint32_t ldg_u8(const uint8_t* p) { return __ldg(p); }
+__device__ __forceinline__ uint32_t ldg_u16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint16_t*>(p)); }
 
-// A CTA per 32 x 32 tile of the output, 32 steps of the contraction at a time through shared
-// memory; thread (x, y) sums out[j0 + y + 8 r, i0 + x], r = 0..3.
-template <int OP, int FMT, bool NV>
-__global__ void __launch_bounds__(256) k_linear_tile(const LinearArgs a)
+// The scale bytes of 32 codes of a row (32-code group grp): one MX byte, or two NV bytes.
+template <bool NV>
+__device__ __forceinline__ uint32_t load_scale(const LinearArgs& a, uint32_t row, uint32_t grp)
 {
-    __shared__ float xs[T][T + 1], qs[T][T + 1];     // [j][c], [i][c]
-    const uint32_t tx = threadIdx.x & 31u, ty = threadIdx.x >> 5;
-    const uint32_t tiles_i = (a.ni + T - 1) / T;
-    const uint32_t i0 = (blockIdx.x % tiles_i) * T, j0 = (blockIdx.x / tiles_i) * T;
-    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(a.x);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t c0 = 0; c0 < a.nc; c0 += T) {
-        for (uint32_t r = ty; r < T; r += 8) {
-            if (OP == LIN_GRAD_WEIGHT) {             // rows are the contraction
-                const uint32_t c = c0 + r, j = j0 + tx, i = i0 + tx;
-                xs[tx][r] = c < a.nc && j < a.nj ? __bfloat162float(x[c * a.ldx + j]) : 0.f;
-                qs[tx][r] = c < a.nc && i < a.ni ? code_value<FMT, NV>(a, c, i) : 0.f;
-            } else {
-                const uint32_t c = c0 + tx, j = j0 + r;
-                xs[r][tx] = c < a.nc && j < a.nj ? __bfloat162float(x[j * a.ldx + c]) : 0.f;
-                if (OP == LIN_FORWARD) {
-                    const uint32_t i = i0 + r;
-                    qs[r][tx] = c < a.nc && i < a.ni ? code_value<FMT, NV>(a, i, c) : 0.f;
-                } else {
-                    const uint32_t cc = c0 + r, i = i0 + tx;
-                    qs[tx][r] = cc < a.nc && i < a.ni ? code_value<FMT, NV>(a, cc, i) : 0.f;
+    return NV ? ldg_u16(a.scales + scale_offset(a, row, 2 * grp)) : ldg_u8(a.scales + scale_offset(a, row, grp));
+}
+
+template <bool NV>
+__device__ __forceinline__ float out_scale(const LinearArgs& a) { return NV ? __fmul_rn(__ldg(a.tensor_scale), NV_OUT) : 1.0f; }
+
+__device__ __forceinline__ void store_out(const LinearArgs& a, size_t o, float v)
+{
+    if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+    else reinterpret_cast<float*>(a.out)[o] = v;
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: y[t, n] for t < 8 MT.
+//
+// A CTA of 8 warps takes 16 R weight rows; the warps share out the columns in pieces of 128
+// (64 bytes of codes), piece after piece in turn, so that together they read runs of 512
+// bytes of a row. A lane (g = lane / 4, q = lane % 4) loads the 32 codes q of rows g and g +
+// 8 of each 16 (16 bytes each) and the 32 values q of token g, and takes the columns in the
+// order in which widening leaves them: an mma.sync adds up 16 columns in any order as long as
+// both operands use the same one. The warps' sums meet in shared memory, in warp order.
+// ---------------------------------------------------------------------------
+
+constexpr int ROWS_WARPS = 8;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ldg_x(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+template <bool NV, int R, int MT>
+__global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArgs a)
+{
+    using W = Widen<BQ_FP4_E2M1, NV>;
+    constexpr uint32_t TS = 16 * R + 4;              // floats from token to token: conflict-free
+    __shared__ float part[ROWS_WARPS][8 * MT * TS];
+    pdl_wait();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g = lane >> 2, q = lane & 3u;
+    const uint32_t row0 = blockIdx.x * (16u * R);
+    const uint32_t groups = a.k / 32u;
+    float acc[R][MT][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[r][t][e] = 0.0f;
+
+    uint32_t rows[2 * R];
+    bool live[2 * R];
+#pragma unroll
+    for (int h = 0; h < 2 * R; ++h) {
+        rows[h] = row0 + 8u * h + g;
+        live[h] = rows[h] < a.ni;
+    }
+    const uint16_t* xr[MT];
+    bool tok[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const uint32_t j = 8u * t + g;
+        tok[t] = j < a.nj;
+        xr[t] = reinterpret_cast<const uint16_t*>(a.x) + (tok[t] ? j : 0u) * a.ldx;
+    }
+
+#pragma unroll 2
+    for (uint32_t grp = 4u * warp + q; grp - q < groups; grp += 4u * ROWS_WARPS) {
+        const bool in = grp < groups;
+        uint32_t w[2 * R][4], s[2 * R];
+#pragma unroll
+        for (int h = 0; h < 2 * R; ++h) {
+            s[h] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[h][i] = 0u;
+            if (in && live[h]) {
+                ld_nc_v4(a.codes + (size_t)rows[h] * (a.k / 2) + grp * 16u, w[h]);
+                s[h] = load_scale<NV>(a, rows[h], grp);
+            }
+        }
+        uint4 x[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[t][i] = in && tok[t] ? ldg_x(xr[t] + grp * 32u + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t p0[16], p1[16];
+            W::pairs(w[2 * r], s[2 * r], p0);
+            W::pairs(w[2 * r + 1], s[2 * r + 1], p1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const uint4 v = x[t][i];         // (e0 e1) (e2 e3) (e4 e5) (e6 e7)
+                    mma_16816(acc[r][t], p0[4 * i], p1[4 * i], p0[4 * i + 1], p1[4 * i + 1],
+                              __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
+                    mma_16816(acc[r][t], p0[4 * i + 2], p1[4 * i + 2], p0[4 * i + 3], p1[4 * i + 3],
+                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 }
             }
         }
-        __syncthreads();
-        for (int c = 0; c < T; ++c)
-            for (int r = 0; r < 4; ++r) acc[r] = __fmaf_rn(xs[ty + 8 * r][c], qs[tx][c], acc[r]);
-        __syncthreads();
     }
-    const float sc = a.tensor_scale ? *a.tensor_scale : 1.0f;
-    const uint32_t i = i0 + tx;
-    for (int r = 0; r < 4; ++r) {
-        const uint32_t j = j0 + ty + 8 * r;
-        if (i >= a.ni || j >= a.nj) continue;
-        const float v = __fmul_rn(acc[r], sc);
-        const size_t o = (size_t)j * a.ni + i;
-        if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
-        else reinterpret_cast<float*>(a.out)[o] = v;
+
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)              // d[e]: row g + 8 (e / 2), token 2 q + e % 2
+                part[warp][(8 * t + 2 * q + (e & 1)) * TS + 16 * r + g + 8 * (e >> 1)] = acc[r][t][e];
+    __syncthreads();
+    const float sc = out_scale<NV>(a);
+    for (uint32_t o = threadIdx.x; o < 8u * MT * 16u * R; o += 32u * ROWS_WARPS) {
+        const uint32_t t = o / (16u * R), i = o % (16u * R);
+        if (t >= a.nj || row0 + i >= a.ni) continue;
+        float v = part[0][t * TS + i];
+#pragma unroll
+        for (int k = 1; k < ROWS_WARPS; ++k) v = __fadd_rn(v, part[k][t * TS + i]);
+        store_out(a, (size_t)t * a.ni + row0 + i, __fmul_rn(v, sc));
     }
 }
 
-template <int OP, int FMT, bool NV>
-cudaError_t run_tile(const LinearArgs& a, cudaStream_t st)
+// ---------------------------------------------------------------------------
+// Tensor cores. out^T in tiles of 128 (i) x bt (j); 64 steps of the contraction per stage:
+//   A: Q widened to bf16, 128 i x 64 c (16 KB), written to shared memory by eight warps from
+//      codes that each thread fetches P stages ahead into registers (32 codes a stage);
+//   B: X by a tensor-map copy, bt j x 64 c.
+// Both with the 128-byte swizzle. Where the stored rows run along the contraction (LIN_FORWARD
+// for both operands, LIN_GRAD_INPUT for X) an operand is K-major: rows of 128 bytes, groups of
+// 8 rows 1024 bytes apart. Where the rows are the contraction (Q of both gradients, X of
+// LIN_GRAD_WEIGHT) it is MN-major: chunks of 64 i (or j) x 64 c, a row of 128 bytes per c, and
+// the tensor cores transpose it. The same threads widen the same 32 codes either way.
+//
+// Warp 0 issues the copies, warp 1 the MMAs (4 of 16 steps a stage, fp32 accumulator in tensor
+// memory, two of them so that a tile's epilogue overlaps the next tile), warps 2-9 widen, warps
+// 10-13 write the accumulator out. A CTA per SM, persistent over the tiles; with fewer tiles
+// than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
+// through distributed shared memory, in rank order: no workspace, and the same sums every time.
+// Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
+// ---------------------------------------------------------------------------
+
+constexpr int MMA_THREADS = 448;
+constexpr int WIDEN_WARPS = 8;
+constexpr int MAX_STAGES = 8;
+constexpr uint32_t A_BYTES = 128u * 128u;
+constexpr uint32_t SMEM_MAX = 232448u;
+constexpr uint32_t ACC_COLS = 256;
+
+struct MmaPlan {
+    uint32_t bt;            // tile width in j: a multiple of 16 (of 64 for LIN_GRAD_WEIGHT), at most 256
+    uint32_t stages;        // of the ring
+    uint32_t tiles_i, tiles;
+    uint32_t kt;            // stages of the contraction (64 steps each)
+    uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
+};
+
+// Instruction descriptor of the bf16 MMA: fp32 accumulator (bits 4-5), bf16 operands (7-9,
+// 10-12), MN-major flags of A and B (15, 16), N / 8 (17-22), M / 16 (24-28).
+template <int OP>
+__device__ __forceinline__ uint32_t mma_desc(uint32_t bt)
 {
-    const uint64_t tiles = (uint64_t)((a.ni + T - 1) / T) * ((a.nj + T - 1) / T);
-    k_linear_tile<OP, FMT, NV><<<(unsigned)tiles, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((OP == LIN_FORWARD ? 0u : 1u) << 15) |
+           ((OP == LIN_GRAD_WEIGHT ? 1u : 0u) << 16) | ((bt >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// MN-major operand: chunks of 64 x 64 (8 KB) side by side, 8 steps 1024 bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr) { return smem_desc(addr, 8192u, 1024u, 2u); }
+
+__device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A float of another CTA's shared memory (addr: the same variable's address in this CTA).
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
+{
+    float v;
+    asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %1, %2;\nld.shared::cluster.f32 %0, [p];\n}"
+                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
+// The stages of a CTA's tiles, one after the other.
+struct Walk {
+    uint32_t tile, kk;      // of the plan's tiles, of the contraction's stages
+};
+
+template <int OP, int FMT, bool NV, int P>
+__global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_constant__ CUtensorMap xmap,
+                                                             const LinearArgs a, const MmaPlan pl)
+{
+    using W = Widen<FMT, NV>;
+    extern __shared__ uint8_t linear_smem[];
+    __shared__ __align__(8) uint64_t a_full[MAX_STAGES], b_full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2],
+        done_bar;
+    __shared__ uint32_t tmem_holder;
+    __shared__ volatile int abort_flag;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t base = (smem_addr(linear_smem) + 1023u) & ~1023u;
+    const uint32_t bt = pl.bt, NS = pl.stages, stage_bytes = A_BYTES + bt * 128u;
+    const uint32_t rank = pl.split > 1 ? cluster_rank() : 0u;
+    // this CTA's tiles and its part of the contraction
+    const uint32_t first = pl.split > 1 ? blockIdx.x / pl.split : blockIdx.x;
+    const uint32_t step = pl.split > 1 ? pl.tiles : gridDim.x;
+    const uint32_t k0 = (uint32_t)((uint64_t)pl.kt * rank / pl.split), k1 = (uint32_t)((uint64_t)pl.kt * (rank + 1) / pl.split);
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < NS; ++s) {
+            mbar_init(smem_addr(&a_full[s]), WIDEN_WARPS);
+            mbar_init(smem_addr(&b_full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&acc_full[b]), 1);
+            mbar_init(smem_addr(&acc_empty[b]), 4);
+        }
+        mbar_init(smem_addr(&done_bar), 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_addr(&tmem_holder)), "r"(2u * ACC_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_holder;
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- X tiles ----
+            uint32_t it = 0;
+            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+                const uint32_t j0 = t / pl.tiles_i * bt;
+                for (uint32_t kk = k0; kk < k1; ++kk, ++it) {
+                    const uint32_t s = it % NS, fb = smem_addr(&b_full[s]);
+                    if (it >= NS && !mbar_wait(smem_addr(&empty[s]), (it / NS - 1) & 1u)) { abort_flag = 1; break; }
+                    if (abort_flag) break;
+                    const uint32_t dst = base + s * stage_bytes + A_BYTES;
+                    mbar_arrive_expect_tx(fb, bt * 128u);
+                    if (OP == LIN_GRAD_WEIGHT) {
+                        for (uint32_t c = 0; c < bt / 64u; ++c)
+                            tma_load_2d(dst + c * 8192u, &xmap, fb, (int)(j0 + 64u * c), (int)(kk * 64u));
+                    } else {
+                        tma_load_2d(dst, &xmap, fb, (int)(kk * 64u), (int)j0);
+                    }
+                }
+            }
+            if (abort_flag) {
+                // let the copies in flight land before the CTA can exit (bounded)
+                const uint32_t from = it > NS ? it - NS : 0u;
+                for (uint32_t j = from; j < it; ++j) (void)mbar_wait(smem_addr(&b_full[j % NS]), (j / NS) & 1u);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- MMAs ----
+            const uint32_t idesc = mma_desc<OP>(bt);
+            uint32_t it = 0, i = 0;
+            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
+                const uint32_t b = i & 1u;
+                if (i >= 2 && !mbar_wait(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + b * ACC_COLS;
+                uint32_t acc = 0;
+                for (uint32_t kk = k0; kk < k1; ++kk, ++it) {
+                    const uint32_t s = it % NS, par = (it / NS) & 1u;
+                    if (!mbar_wait(smem_addr(&b_full[s]), par) || !mbar_wait(smem_addr(&a_full[s]), par)) { abort_flag = 1; break; }
+                    if (abort_flag) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t sa = base + s * stage_bytes, sb = sa + A_BYTES;
+                    const uint64_t ad = OP == LIN_FORWARD ? operand_desc(sa) : mn_desc(sa);
+                    const uint64_t bd = OP == LIN_GRAD_WEIGHT ? mn_desc(sb) : operand_desc(sb);
+                    // 16 steps: 32 bytes along a K-major row, 16 rows (2 KB) of an MN-major chunk
+                    constexpr uint32_t ka = OP == LIN_FORWARD ? 2u : 128u, kb = OP == LIN_GRAD_WEIGHT ? 128u : 2u;
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) {
+                        tc_mma_bf16(d, ad + ka * k, bd + kb * k, idesc, acc);
+                        acc = 1;
+                    }
+                    tc_commit(smem_addr(&empty[s]));
+                }
+                if (abort_flag) break;
+                tc_commit(smem_addr(&acc_full[b]));
+            }
+            // every MMA issued so far completes before done_bar's phase does
+            tc_commit(smem_addr(&done_bar));
+            if (!mbar_wait(smem_addr(&done_bar), 0u)) abort_flag = 1;
+        }
+    } else if (warp < 2 + WIDEN_WARPS) {
+        // ---- Q tiles: thread r, part h takes 32 codes of stored row r (forward: of columns 32 h
+        // of the stage; gradients: of columns 32 h of the tile) ----
+        const uint32_t tid = threadIdx.x - 64u;
+        const uint32_t r = OP == LIN_FORWARD ? tid & 127u : tid & 63u, h = OP == LIN_FORWARD ? tid >> 7 : tid >> 6;
+        const uint32_t row_off = (OP == LIN_FORWARD ? 0u : (h >> 1) * 8192u) + r * 128u;
+        const uint32_t c16 = OP == LIN_FORWARD ? 4u * h : 4u * (h & 1u);     // its first 16-byte unit of the row
+        const uint32_t row_bytes = Fmt<FMT>::four ? a.k / 2u : a.k, grp_bytes = Fmt<FMT>::four ? 16u : 32u;
+        const uint32_t groups = a.k / 32u;
+        const uint32_t my_tiles = first < pl.tiles ? (pl.tiles - first + step - 1u) / step : 0u;
+        const uint64_t total = (uint64_t)my_tiles * (k1 - k0);
+        Walk ld{first, k0};
+        uint32_t w[P][W::WORDS], sc[P];
+        auto fetch = [&](uint32_t (&cw)[W::WORDS], uint32_t& cs) {
+            cs = 0u;
+#pragma unroll
+            for (int e = 0; e < W::WORDS; ++e) cw[e] = 0u;
+            if (ld.tile < pl.tiles) {
+                const uint32_t i0 = ld.tile % pl.tiles_i * 128u;
+                const uint32_t row = OP == LIN_FORWARD ? i0 + r : ld.kk * 64u + r;
+                const uint32_t grp = OP == LIN_FORWARD ? ld.kk * 2u + h : i0 / 32u + h;
+                if (row < a.q_rows && grp < groups) {
+                    const uint8_t* p = a.codes + (size_t)row * row_bytes + (size_t)grp * grp_bytes;
+                    if constexpr (W::WORDS == 4) ld_nc_v4(p, cw);
+                    else ld_nc_v8(p, cw);
+                    cs = load_scale<NV>(a, row, grp);
+                }
+                if (++ld.kk == k1) { ld.kk = k0; ld.tile += step; }
+            }
+        };
+#pragma unroll
+        for (int p = 0; p < P; ++p) fetch(w[p], sc[p]);
+        uint32_t s = 0, round = 0;
+        bool ok = true;
+        for (uint64_t it = 0; it < total && ok; it += P) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                if (it + p >= total || !ok) continue;
+                uint32_t v[W::WORDS * W::RAW], o[16];
+                W::pairs(w[p], sc[p], v);
+                W::in_order(v, o);
+                fetch(w[p], sc[p]);
+                if (round > 0) {
+                    ok = mbar_wait(smem_addr(&empty[s]), (round - 1) & 1u);
+                    ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
+                    if (!ok) { abort_flag = 1; continue; }
+                }
+                const uint32_t dst = base + s * stage_bytes + row_off;
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    sts_v4(dst + (((c16 + e) ^ (r & 7u)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&a_full[s]));
+                if (++s == NS) { s = 0; ++round; }
+            }
+        }
+    } else {
+        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, i.e. 32 i ----
+        const uint32_t q = warp & 3u, il = q * 32u + lane;
+        const float sc = out_scale<NV>(a);
+        uint32_t n = 0;
+        for (uint32_t t = first; t < pl.tiles; t += step, ++n) {
+            const uint32_t b = n & 1u;
+            bool ok = mbar_wait(smem_addr(&acc_full[b]), (n / 2) & 1u);
+            ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
+            if (!ok) { abort_flag = 1; break; }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t i = t % pl.tiles_i * 128u + il, j0 = t / pl.tiles_i * bt;
+            const uint32_t cols = min(bt, a.nj - j0);
+            for (uint32_t c0 = 0; c0 < cols; c0 += 32u) {
+                uint32_t v[32];
+                tmem_ld32(tmem + b * ACC_COLS + ((q * 32u) << 16) + c0, v);
+                if (pl.split > 1) {
+                    // this CTA's part of the sums, [j][i], over the stages (all consumed)
+#pragma unroll
+                    for (uint32_t e = 0; e < 32; ++e)
+                        if (c0 + e < bt)
+                            asm volatile("st.shared.b32 [%0], %1;" :: "r"(base + ((c0 + e) * 128u + il) * 4u), "r"(v[e]) : "memory");
+                } else if (i < a.ni) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 32; ++e)
+                        if (c0 + e < cols)
+                            store_out(a, (size_t)(j0 + c0 + e) * a.ni + i, NV ? __fmul_rn(__uint_as_float(v[e]), sc) : __uint_as_float(v[e]));
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
+        }
+    }
+    __syncwarp();
+    if (pl.split > 1) {
+        cluster_sync();
+        // every CTA of the cluster adds up the parts of its share of the columns
+        const uint32_t i = first % pl.tiles_i * 128u, j0 = first / pl.tiles_i * bt;
+        const uint32_t from = bt * rank / pl.split, to = min(bt * (rank + 1) / pl.split, a.nj - j0);
+        const float sc = out_scale<NV>(a);
+        for (uint32_t o = from * 128u + threadIdx.x; o < to * 128u; o += MMA_THREADS) {
+            const uint32_t ii = i + (o & 127u);
+            if (ii >= a.ni) continue;
+            float v = 0.0f;
+            for (uint32_t rk = 0; rk < pl.split; ++rk) v = __fadd_rn(v, ld_cluster(base + o * 4u, rk));
+            store_out(a, (size_t)(j0 + (o >> 7)) * a.ni + ii, NV ? __fmul_rn(v, sc) : v);
+        }
+        cluster_sync();                              // no CTA leaves while its parts are being read
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0 && abort_flag) atomicAdd(&g_linear_wait_timeouts, 1u);
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2u * ACC_COLS) : "memory");
+    }
+}
+
+// x as stored, boxes of 64 columns (128 bytes) x box_rows rows, 128-byte swizzle; what lies
+// outside the matrix arrives as zeros.
+cudaError_t x_map(const LinearArgs& a, uint32_t box_rows, CUtensorMap* map)
+{
+    *map = CUtensorMap{};
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {a.x_cols, a.x_rows};
+    const cuuint64_t strides[1] = {a.ldx * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.x), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
+
+// The tile width that takes the fewest rounds of tiles over the SMs, weighed by a round's
+// length (a stage costs bt, and no less than the 128 that widening its codes takes); then a
+// split of the contraction while tiles leave SMs idle and every part keeps four stages.
+MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
+{
+    MmaPlan p;
+    const uint32_t unit = op == LIN_GRAD_WEIGHT ? 64u : 16u;
+    p.tiles_i = ceil_div(a.ni, 128u);
+    p.kt = ceil_div(a.nc, 64u);
+    const uint32_t most = std::min(256u, ceil_div(a.nj, unit) * unit);
+    uint64_t best = ~0ull;
+    p.bt = most;
+    for (uint32_t bt = most; bt >= unit && (bt >= 128u || bt == most); bt -= unit) {
+        const uint64_t tiles = (uint64_t)p.tiles_i * ceil_div(a.nj, bt);
+        const uint64_t cost = ((tiles + sms - 1) / sms) * std::max(bt, 128u);
+        if (cost < best) { best = cost; p.bt = bt; }
+    }
+    p.tiles = p.tiles_i * ceil_div(a.nj, p.bt);
+    p.split = 1;
+    while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.kt >= p.split * 2 * 4) p.split *= 2;
+    p.stages = std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 1024u - 1024u) / (A_BYTES + p.bt * 128u));
+    return p;
+}
+
+template <int OP, int FMT, bool NV>
+cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
+{
+    constexpr int P = Fmt<FMT>::four ? 4 : 2;
+    constexpr auto kern = k_linear_mma<OP, FMT, NV, P>;
+    static std::atomic<uint64_t> attr_set{0};        // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_set.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(SMEM_MAX - 1024u));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const uint32_t sms = (uint32_t)device_sm_count();
+    const MmaPlan pl = make_mma_plan(OP, a, sms);
+    CUtensorMap xm;
+    e = x_map(a, OP == LIN_GRAD_WEIGHT ? 64u : pl.bt, &xm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(pl.split > 1 ? pl.tiles * pl.split : std::min(pl.tiles, sms));
+    cfg.blockDim = dim3(MMA_THREADS);
+    cfg.dynamicSmemBytes = pl.stages * (A_BYTES + pl.bt * 128u) + 1024u;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = pl.split;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pl.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, xm, a, pl);
+}
+
+template <bool NV, int R>
+cudaError_t run_rows(const LinearArgs& a, cudaStream_t st)
+{
+    const unsigned grid = ceil_div(a.ni, 16u * R);
+    return a.nj <= 8 ? launch_pdl(k_linear_rows<NV, R, 1>, grid, 32 * ROWS_WARPS, 0, st, a)
+                     : launch_pdl(k_linear_rows<NV, R, 2>, grid, 32 * ROWS_WARPS, 0, st, a);
+}
+
+template <bool NV>
+cudaError_t run_forward(const LinearArgs& a, cudaStream_t st)
+{
+    if (a.nj > 16) return run_mma<LIN_FORWARD, BQ_FP4_E2M1, NV>(a, st);
+    // two CTAs per SM at 32 rows each, else 16 rows so that every SM has work
+    return ceil_div(a.ni, 32u) >= 2u * (uint32_t)device_sm_count() ? run_rows<NV, 2>(a, st) : run_rows<NV, 1>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(int op, int fmt, bool nv, const LinearArgs& a, cudaStream_t st)
 {
-    if (op == LIN_FORWARD)
-        return nv ? run_tile<LIN_FORWARD, BQ_FP4_E2M1, true>(a, st) : run_tile<LIN_FORWARD, BQ_FP4_E2M1, false>(a, st);
+    if (op == LIN_FORWARD) return nv ? run_forward<true>(a, st) : run_forward<false>(a, st);
     if (op == LIN_GRAD_INPUT)
-        return nv ? run_tile<LIN_GRAD_INPUT, BQ_FP4_E2M1, true>(a, st)
-                  : run_tile<LIN_GRAD_INPUT, BQ_FP4_E2M1, false>(a, st);
-    if (fmt == BQ_FP8_E4M3) return run_tile<LIN_GRAD_WEIGHT, BQ_FP8_E4M3, false>(a, st);
-    if (fmt == BQ_FP8_E5M2) return run_tile<LIN_GRAD_WEIGHT, BQ_FP8_E5M2, false>(a, st);
-    if (fmt == BQ_INT8_SYM) return run_tile<LIN_GRAD_WEIGHT, BQ_INT8_SYM, false>(a, st);
+        return nv ? run_mma<LIN_GRAD_INPUT, BQ_FP4_E2M1, true>(a, st) : run_mma<LIN_GRAD_INPUT, BQ_FP4_E2M1, false>(a, st);
+    if (fmt == BQ_FP8_E4M3) return run_mma<LIN_GRAD_WEIGHT, BQ_FP8_E4M3, false>(a, st);
+    if (fmt == BQ_FP8_E5M2) return run_mma<LIN_GRAD_WEIGHT, BQ_FP8_E5M2, false>(a, st);
+    if (fmt == BQ_INT8_SYM) return run_mma<LIN_GRAD_WEIGHT, BQ_INT8_SYM, false>(a, st);
     return cudaErrorInvalidValue;
 }
 
-cudaError_t linear_wait_timeouts(unsigned int* count, bool)
+cudaError_t linear_wait_timeouts(unsigned int* count, bool reset)
 {
-    *count = 0;
-    return cudaSuccess;
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_linear_wait_timeouts, sizeof(unsigned int));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0u;
+        e = cudaMemcpyToSymbol(g_linear_wait_timeouts, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 }  // namespace bq
