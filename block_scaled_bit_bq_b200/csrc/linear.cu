@@ -35,14 +35,51 @@ __device__ __forceinline__ size_t scale_offset(const LinearArgs& a, uint32_t row
     return a.gemm_layout ? (size_t)gemm_scale_offset(row, blk, a.nb) : (size_t)row * a.nb + blk;
 }
 
-__device__ __forceinline__ uint32_t ldg_u8(const uint8_t* p) { return __ldg(p); }
-__device__ __forceinline__ uint32_t ldg_u16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint16_t*>(p)); }
+// Scale loads as volatile asm: they stay where they are issued, ahead of the codes' use (as
+// plain loads the compiler moves them down to it, and each one's latency shows).
+__device__ __forceinline__ uint32_t ldg_u8(const uint8_t* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ldg_u16(const uint8_t* p)
+{
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ldg_u32(const uint8_t* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 
 // The scale bytes of 32 codes of a row (32-code group grp): one MX byte, or two NV bytes.
 template <bool NV>
 __device__ __forceinline__ uint32_t load_scale(const LinearArgs& a, uint32_t row, uint32_t grp)
 {
     return NV ? ldg_u16(a.scales + scale_offset(a, row, 2 * grp)) : ldg_u8(a.scales + scale_offset(a, row, grp));
+}
+
+// The same of two 32-code groups, grp (even) and grp + 1, the second where it exists: in one
+// load where a row's scales start on a multiple of its size (wide).
+template <bool NV>
+__device__ __forceinline__ void load_scale_pair(const LinearArgs& a, uint32_t row, uint32_t grp, bool wide, bool second,
+                                                uint32_t (&s)[2])
+{
+    const uint8_t* p = a.scales + scale_offset(a, row, NV ? 2 * grp : grp);
+    if (wide) {
+        const uint32_t v = NV ? ldg_u32(p) : ldg_u16(p);
+        s[0] = NV ? v & 0xFFFFu : v & 0xFFu;
+        s[1] = NV ? v >> 16 : v >> 8;
+    } else {
+        s[0] = NV ? ldg_u16(p) : ldg_u8(p);
+        if (second) s[1] = NV ? ldg_u16(p + 2) : ldg_u8(p + 1);
+    }
 }
 
 template <bool NV>
@@ -52,6 +89,22 @@ __device__ __forceinline__ void store_out(const LinearArgs& a, size_t o, float v
 {
     if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
     else reinterpret_cast<float*>(a.out)[o] = v;
+}
+
+// n (at most 32) values of one column i of out, rows apart, the first at element o; times sc.
+__device__ __forceinline__ void store_column(const LinearArgs& a, size_t o, uint32_t n, const uint32_t (&v)[32], float sc)
+{
+    if (a.out_bf16) {
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
+#pragma unroll
+        for (uint32_t e = 0; e < 32; ++e, p += a.ni)
+            if (e < n) *p = __float2bfloat16_rn(__fmul_rn(__uint_as_float(v[e]), sc));
+    } else {
+        float* p = reinterpret_cast<float*>(a.out) + o;
+#pragma unroll
+        for (uint32_t e = 0; e < 32; ++e, p += a.ni)
+            if (e < n) *p = __fmul_rn(__uint_as_float(v[e]), sc);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -76,9 +129,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg_x(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint4 ldg_x(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 
-template <bool NV, int R, int MT>
+template <bool NV, int R, int MT, int D>
 __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArgs a)
 {
     using W = Widen<BQ_FP4_E2M1, NV>;
@@ -112,42 +170,52 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
         xr[t] = reinterpret_cast<const uint16_t*>(a.x) + (tok[t] ? j : 0u) * a.ldx;
     }
 
-#pragma unroll 2
-    for (uint32_t grp = 4u * warp + q; grp - q < groups; grp += 4u * ROWS_WARPS) {
+    // the loads of D pieces ahead of the one being multiplied
+    uint32_t w[D][2 * R][4], s[D][2 * R];
+    uint4 x[D][MT][4];
+    auto fetch = [&](uint32_t grp, uint32_t (&cw)[2 * R][4], uint32_t (&cs)[2 * R], uint4 (&cx)[MT][4]) {
         const bool in = grp < groups;
-        uint32_t w[2 * R][4], s[2 * R];
 #pragma unroll
         for (int h = 0; h < 2 * R; ++h) {
-            s[h] = 0u;
+            cs[h] = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[h][i] = 0u;
+            for (int i = 0; i < 4; ++i) cw[h][i] = 0u;
             if (in && live[h]) {
-                ld_nc_v4(a.codes + (size_t)rows[h] * (a.k / 2) + grp * 16u, w[h]);
-                s[h] = load_scale<NV>(a, rows[h], grp);
+                ld_nc_v4(a.codes + (size_t)rows[h] * (a.k / 2) + grp * 16u, cw[h]);
+                cs[h] = load_scale<NV>(a, rows[h], grp);
             }
         }
-        uint4 x[MT][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[t][i] = in && tok[t] ? ldg_x(xr[t] + grp * 32u + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                cx[t][i] = in && tok[t] ? ldg_x(xr[t] + grp * 32u + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    constexpr uint32_t STEP = 4u * ROWS_WARPS;
+    const uint32_t g0 = 4u * warp + q;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            uint32_t p0[16], p1[16];
-            W::pairs(w[2 * r], s[2 * r], p0);
-            W::pairs(w[2 * r + 1], s[2 * r + 1], p1);
+    for (int p = 0; p < D; ++p) fetch(g0 + p * STEP, w[p], s[p], x[p]);
+    for (uint32_t grp = g0; grp - q < groups; grp += D * STEP) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int p = 0; p < D; ++p) {
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const uint4 v = x[t][i];         // (e0 e1) (e2 e3) (e4 e5) (e6 e7)
-                    mma_16816(acc[r][t], p0[4 * i], p1[4 * i], p0[4 * i + 1], p1[4 * i + 1],
-                              __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
-                    mma_16816(acc[r][t], p0[4 * i + 2], p1[4 * i + 2], p0[4 * i + 3], p1[4 * i + 3],
-                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            for (int r = 0; r < R; ++r) {
+                uint32_t p0[16], p1[16];
+                W::pairs(w[p][2 * r], s[p][2 * r], p0);
+                W::pairs(w[p][2 * r + 1], s[p][2 * r + 1], p1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const uint4 v = x[p][t][i];      // (e0 e1) (e2 e3) (e4 e5) (e6 e7)
+                        mma_16816(acc[r][t], p0[4 * i], p1[4 * i], p0[4 * i + 1], p1[4 * i + 1],
+                                  __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
+                        mma_16816(acc[r][t], p0[4 * i + 2], p1[4 * i + 2], p0[4 * i + 3], p1[4 * i + 3],
+                                  __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+                    }
                 }
             }
+            fetch(grp + (D + p) * STEP, w[p], s[p], x[p]);
         }
     }
 
@@ -172,25 +240,27 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 
 // ---------------------------------------------------------------------------
 // Tensor cores. out^T in tiles of 128 (i) x bt (j); 64 steps of the contraction per stage:
-//   A: Q widened to bf16, 128 i x 64 c (16 KB), written to shared memory by eight warps from
-//      codes that each thread fetches P stages ahead into registers (32 codes a stage);
+//   A: Q widened to bf16, 128 i x 64 c (16 KB), written to shared memory by the widening warps:
+//      four groups of four warps take the stages in turn, a thread 64 codes of one stored row,
+//      which it fetched into registers P of its stages before;
 //   B: X by a tensor-map copy, bt j x 64 c.
 // Both with the 128-byte swizzle. Where the stored rows run along the contraction (LIN_FORWARD
 // for both operands, LIN_GRAD_INPUT for X) an operand is K-major: rows of 128 bytes, groups of
 // 8 rows 1024 bytes apart. Where the rows are the contraction (Q of both gradients, X of
 // LIN_GRAD_WEIGHT) it is MN-major: chunks of 64 i (or j) x 64 c, a row of 128 bytes per c, and
-// the tensor cores transpose it. The same threads widen the same 32 codes either way.
+// the tensor cores transpose it. Either way a thread's 64 values are one row of 128 bytes.
 //
 // Warp 0 issues the copies, warp 1 the MMAs (4 of 16 steps a stage, fp32 accumulator in tensor
-// memory, two of them so that a tile's epilogue overlaps the next tile), warps 2-9 widen, warps
-// 10-13 write the accumulator out. A CTA per SM, persistent over the tiles; with fewer tiles
+// memory, two of them so that a tile's epilogue overlaps the next tile), warps 2-17 widen, warps
+// 18-21 write the accumulator out. A CTA per SM, persistent over the tiles; with fewer tiles
 // than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
 // through distributed shared memory, in rank order: no workspace, and the same sums every time.
 // Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
 // ---------------------------------------------------------------------------
 
-constexpr int MMA_THREADS = 448;
-constexpr int WIDEN_WARPS = 8;
+constexpr uint32_t WIDEN_GROUPS = 4, GROUP_WARPS = 4, GROUP_THREADS = 32 * GROUP_WARPS;
+constexpr uint32_t WIDEN_WARPS = WIDEN_GROUPS * GROUP_WARPS;
+constexpr int MMA_THREADS = 32 * (2 + WIDEN_WARPS + 4);
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t A_BYTES = 128u * 128u;
 constexpr uint32_t SMEM_MAX = 232448u;
@@ -198,9 +268,10 @@ constexpr uint32_t ACC_COLS = 256;
 
 struct MmaPlan {
     uint32_t bt;            // tile width in j: a multiple of 16 (of 64 for LIN_GRAD_WEIGHT), at most 256
+    uint32_t subs;          // 64-step parts of a stage: 1 or 2
     uint32_t stages;        // of the ring
     uint32_t tiles_i, tiles;
-    uint32_t kt;            // stages of the contraction (64 steps each)
+    uint32_t kt;            // stages of the contraction
     uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
 };
 
@@ -221,6 +292,14 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, 
     asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0u;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -244,24 +323,19 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     return v;
 }
 
-// The stages of a CTA's tiles, one after the other.
-struct Walk {
-    uint32_t tile, kk;      // of the plan's tiles, of the contraction's stages
-};
-
 template <int OP, int FMT, bool NV, int P>
 __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_constant__ CUtensorMap xmap,
                                                              const LinearArgs a, const MmaPlan pl)
 {
     using W = Widen<FMT, NV>;
     extern __shared__ uint8_t linear_smem[];
-    __shared__ __align__(8) uint64_t a_full[MAX_STAGES], b_full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2],
-        done_bar;
+    __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], done_bar;
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t base = (smem_addr(linear_smem) + 1023u) & ~1023u;
-    const uint32_t bt = pl.bt, NS = pl.stages, stage_bytes = A_BYTES + bt * 128u;
+    const uint32_t bt = pl.bt, subs = pl.subs, NS = pl.stages;
+    const uint32_t b_bytes = bt * 128u, sub_bytes = A_BYTES + b_bytes, stage_bytes = subs * sub_bytes;
     const uint32_t rank = pl.split > 1 ? cluster_rank() : 0u;
     // this CTA's tiles and its part of the contraction
     const uint32_t first = pl.split > 1 ? blockIdx.x / pl.split : blockIdx.x;
@@ -270,8 +344,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < NS; ++s) {
-            mbar_init(smem_addr(&a_full[s]), WIDEN_WARPS);
-            mbar_init(smem_addr(&b_full[s]), 1);
+            mbar_init(smem_addr(&full[s]), subs * GROUP_WARPS + 1u);     // the widening warps, and the copies
             mbar_init(smem_addr(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -294,121 +367,152 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- X tiles ----
-            uint32_t it = 0;
-            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
-                const uint32_t j0 = t / pl.tiles_i * bt;
-                for (uint32_t kk = k0; kk < k1; ++kk, ++it) {
-                    const uint32_t s = it % NS, fb = smem_addr(&b_full[s]);
-                    if (it >= NS && !mbar_wait(smem_addr(&empty[s]), (it / NS - 1) & 1u)) { abort_flag = 1; break; }
-                    if (abort_flag) break;
-                    const uint32_t dst = base + s * stage_bytes + A_BYTES;
-                    mbar_arrive_expect_tx(fb, bt * 128u);
-                    if (OP == LIN_GRAD_WEIGHT) {
-                        for (uint32_t c = 0; c < bt / 64u; ++c)
-                            tma_load_2d(dst + c * 8192u, &xmap, fb, (int)(j0 + 64u * c), (int)(kk * 64u));
-                    } else {
-                        tma_load_2d(dst, &xmap, fb, (int)(kk * 64u), (int)j0);
+        // ---- X tiles ----
+        const bool leader = elect_one();
+        uint32_t s = 0, round = 0;                   // slot of the ring, and how often it wrapped
+        for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+            const int j0 = (int)(t / pl.tiles_i * bt);
+            for (uint32_t kk = k0; kk < k1; ++kk) {
+                if (round > 0 && !mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u)) { abort_flag = 1; break; }
+                if (abort_flag) break;
+                if (leader) {
+                    const uint32_t fb = smem_addr(&full[s]);
+                    uint32_t dst = base + s * stage_bytes + A_BYTES;
+                    mbar_arrive_expect_tx(fb, subs * b_bytes);
+                    for (uint32_t u = 0; u < subs; ++u, dst += sub_bytes) {
+                        const int c = (int)((kk * subs + u) * 64u);
+                        if (OP == LIN_GRAD_WEIGHT) {
+                            for (uint32_t x = 0; x < bt / 64u; ++x)
+                                tma_load_2d(dst + x * 8192u, &xmap, fb, j0 + (int)(64u * x), c);
+                        } else {
+                            tma_load_2d(dst, &xmap, fb, c, j0);
+                        }
                     }
                 }
+                __syncwarp();
+                if (++s == NS) { s = 0; ++round; }
             }
-            if (abort_flag) {
-                // let the copies in flight land before the CTA can exit (bounded)
-                const uint32_t from = it > NS ? it - NS : 0u;
-                for (uint32_t j = from; j < it; ++j) (void)mbar_wait(smem_addr(&b_full[j % NS]), (j / NS) & 1u);
-            }
+        }
+        // the copies in flight (at most one stage a slot) land before the CTA can exit: after an
+        // abort the full barriers may stay short of the widening warps' arrivals, so the wait
+        // (bounded) is for their time only
+        if (abort_flag) {
+            for (uint32_t j = 0; j < NS && (round > 0 || j < s); ++j)
+                (void)mbar_wait(smem_addr(&full[j]), (j < s ? round : round - 1) & 1u);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---- MMAs ----
-            const uint32_t idesc = mma_desc<OP>(bt);
-            uint32_t it = 0, i = 0;
-            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
-                const uint32_t b = i & 1u;
-                if (i >= 2 && !mbar_wait(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t d = tmem + b * ACC_COLS;
-                uint32_t acc = 0;
-                for (uint32_t kk = k0; kk < k1; ++kk, ++it) {
-                    const uint32_t s = it % NS, par = (it / NS) & 1u;
-                    if (!mbar_wait(smem_addr(&b_full[s]), par) || !mbar_wait(smem_addr(&a_full[s]), par)) { abort_flag = 1; break; }
-                    if (abort_flag) break;
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t sa = base + s * stage_bytes, sb = sa + A_BYTES;
-                    const uint64_t ad = OP == LIN_FORWARD ? operand_desc(sa) : mn_desc(sa);
-                    const uint64_t bd = OP == LIN_GRAD_WEIGHT ? mn_desc(sb) : operand_desc(sb);
-                    // 16 steps: 32 bytes along a K-major row, 16 rows (2 KB) of an MN-major chunk
-                    constexpr uint32_t ka = OP == LIN_FORWARD ? 2u : 128u, kb = OP == LIN_GRAD_WEIGHT ? 128u : 2u;
-#pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) {
-                        tc_mma_bf16(d, ad + ka * k, bd + kb * k, idesc, acc);
-                        acc = 1;
-                    }
-                    tc_commit(smem_addr(&empty[s]));
-                }
+        // ---- MMAs: 16 steps are 32 bytes along a K-major row, 16 rows (2 KB) of an MN-major
+        // chunk. The whole warp runs the loop, so that descriptors stay in uniform registers ----
+        constexpr uint32_t ka = OP == LIN_FORWARD ? 2u : 128u, kb = OP == LIN_GRAD_WEIGHT ? 128u : 2u;
+        const bool leader = elect_one();
+        const uint32_t idesc = mma_desc<OP>(bt);
+        const uint64_t ad0 = OP == LIN_FORWARD ? operand_desc(base) : mn_desc(base);
+        const uint64_t bd0 = OP == LIN_GRAD_WEIGHT ? mn_desc(base + A_BYTES) : operand_desc(base + A_BYTES);
+        uint32_t s = 0, par = 0, i = 0;
+        for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
+            const uint32_t b = i & 1u;
+            if (i >= 2 && !mbar_wait_ring(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + b * ACC_COLS;
+            uint32_t acc = 0;
+            for (uint32_t kk = k0; kk < k1; ++kk) {
+                if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
                 if (abort_flag) break;
-                tc_commit(smem_addr(&acc_full[b]));
-            }
-            // every MMA issued so far completes before done_bar's phase does
-            tc_commit(smem_addr(&done_bar));
-            if (!mbar_wait(smem_addr(&done_bar), 0u)) abort_flag = 1;
-        }
-    } else if (warp < 2 + WIDEN_WARPS) {
-        // ---- Q tiles: thread r, part h takes 32 codes of stored row r (forward: of columns 32 h
-        // of the stage; gradients: of columns 32 h of the tile) ----
-        const uint32_t tid = threadIdx.x - 64u;
-        const uint32_t r = OP == LIN_FORWARD ? tid & 127u : tid & 63u, h = OP == LIN_FORWARD ? tid >> 7 : tid >> 6;
-        const uint32_t row_off = (OP == LIN_FORWARD ? 0u : (h >> 1) * 8192u) + r * 128u;
-        const uint32_t c16 = OP == LIN_FORWARD ? 4u * h : 4u * (h & 1u);     // its first 16-byte unit of the row
-        const uint32_t row_bytes = Fmt<FMT>::four ? a.k / 2u : a.k, grp_bytes = Fmt<FMT>::four ? 16u : 32u;
-        const uint32_t groups = a.k / 32u;
-        const uint32_t my_tiles = first < pl.tiles ? (pl.tiles - first + step - 1u) / step : 0u;
-        const uint64_t total = (uint64_t)my_tiles * (k1 - k0);
-        Walk ld{first, k0};
-        uint32_t w[P][W::WORDS], sc[P];
-        auto fetch = [&](uint32_t (&cw)[W::WORDS], uint32_t& cs) {
-            cs = 0u;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (uint32_t u = 0; u < subs; ++u) {
+                    const uint64_t so = (s * stage_bytes + u * sub_bytes) >> 4, ad = ad0 + so, bd = bd0 + so;
+                    if (leader) {
 #pragma unroll
-            for (int e = 0; e < W::WORDS; ++e) cw[e] = 0u;
-            if (ld.tile < pl.tiles) {
-                const uint32_t i0 = ld.tile % pl.tiles_i * 128u;
-                const uint32_t row = OP == LIN_FORWARD ? i0 + r : ld.kk * 64u + r;
-                const uint32_t grp = OP == LIN_FORWARD ? ld.kk * 2u + h : i0 / 32u + h;
+                        for (uint32_t k = 0; k < 4; ++k) tc_mma_bf16(d, ad + ka * k, bd + kb * k, idesc, k ? 1u : acc);
+                    }
+                    acc = 1;
+                }
+                if (leader) tc_commit(smem_addr(&empty[s]));
+                __syncwarp();
+                if (++s == NS) { s = 0; par ^= 1u; }
+            }
+            if (abort_flag) break;
+            if (leader) tc_commit(smem_addr(&acc_full[b]));
+            __syncwarp();
+        }
+        // every MMA issued so far completes before done_bar's phase does
+        if (leader) tc_commit(smem_addr(&done_bar));
+        __syncwarp();
+        if (!mbar_wait(smem_addr(&done_bar), 0u)) abort_flag = 1;
+    } else if (warp < 2 + WIDEN_WARPS) {
+        // ---- Q tiles: a thread takes 64 codes of one stored row: forward, row r of the tile and
+        // the part's columns; gradients, row r of the part and half h of the tile's columns.
+        // Group g takes parts g, g + 4, ... of this CTA's run of 64-step parts ----
+        const uint32_t grp_id = (warp - 2u) / GROUP_WARPS, tid = (threadIdx.x - 64u) % GROUP_THREADS;
+        const uint32_t r = OP == LIN_FORWARD ? tid : tid & 63u, h = OP == LIN_FORWARD ? 0u : tid >> 6;
+        const uint32_t row_off = h * 8192u + r * 128u;
+        const uint32_t row_bytes = Fmt<FMT>::four ? a.k / 2u : a.k;
+        constexpr uint32_t grp_bytes = Fmt<FMT>::four ? 16u : 32u;
+        const uint32_t groups = a.k / 32u, kts = (k1 - k0) * subs;   // parts of 64 steps per tile
+        const bool wide = a.gemm_layout || (NV ? a.nb % 4u == 0 : a.nb % 2u == 0);
+        uint32_t ld_tile = first, ld_kk = grp_id;            // the next part to fetch
+        uint32_t w[P][2][W::WORDS], sc[P][2];
+        auto fetch = [&](uint32_t (&cw)[2][W::WORDS], uint32_t (&cs)[2]) {
+            while (ld_kk >= kts && ld_tile < pl.tiles) { ld_kk -= kts; ld_tile += step; }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                cs[x] = 0u;
+#pragma unroll
+                for (int e = 0; e < W::WORDS; ++e) cw[x][e] = 0u;
+            }
+            if (ld_tile < pl.tiles) {
+                const uint32_t i0 = ld_tile % pl.tiles_i * 128u, kk = k0 * subs + ld_kk;
+                const uint32_t row = OP == LIN_FORWARD ? i0 + r : kk * 64u + r;
+                const uint32_t grp = OP == LIN_FORWARD ? kk * 2u : i0 / 32u + 2u * h;
                 if (row < a.q_rows && grp < groups) {
                     const uint8_t* p = a.codes + (size_t)row * row_bytes + (size_t)grp * grp_bytes;
-                    if constexpr (W::WORDS == 4) ld_nc_v4(p, cw);
-                    else ld_nc_v8(p, cw);
-                    cs = load_scale<NV>(a, row, grp);
+                    const bool second = grp + 1u < groups;
+                    if constexpr (W::WORDS == 4) {
+                        ld_nc_v4(p, cw[0]);
+                        if (second) ld_nc_v4(p + 16, cw[1]);
+                    } else {
+                        ld_nc_v8(p, cw[0]);
+                        if (second) ld_nc_v8(p + 32, cw[1]);
+                    }
+                    load_scale_pair<NV>(a, row, grp, wide, second, cs);
                 }
-                if (++ld.kk == k1) { ld.kk = k0; ld.tile += step; }
             }
+            ld_kk += WIDEN_GROUPS;
         };
 #pragma unroll
         for (int p = 0; p < P; ++p) fetch(w[p], sc[p]);
-        uint32_t s = 0, round = 0;
+        const uint32_t my_tiles = (pl.tiles - first + step - 1u) / step;
+        const uint64_t total = (uint64_t)my_tiles * kts;
+        uint32_t s = grp_id / subs, round = 0;               // NS * subs >= 4: no group starts past the ring
+        const uint32_t sub = grp_id % subs, hop = WIDEN_GROUPS / subs;
         bool ok = true;
-        for (uint64_t it = 0; it < total && ok; it += P) {
+        for (uint64_t it = grp_id; it < total && ok; it += P * WIDEN_GROUPS) {
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                if (it + p >= total || !ok) continue;
-                uint32_t v[W::WORDS * W::RAW], o[16];
-                W::pairs(w[p], sc[p], v);
-                W::in_order(v, o);
+                if (it + p * WIDEN_GROUPS >= total || !ok) continue;
+                uint32_t o[2][16];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t v[W::WORDS * W::RAW];
+                    W::pairs(w[p][x], sc[p][x], v);
+                    W::in_order(v, o[x]);
+                }
                 fetch(w[p], sc[p]);
                 if (round > 0) {
-                    ok = mbar_wait(smem_addr(&empty[s]), (round - 1) & 1u);
+                    ok = mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u);
                     ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
                     if (!ok) { abort_flag = 1; continue; }
                 }
-                const uint32_t dst = base + s * stage_bytes + row_off;
+                const uint32_t dst = base + s * stage_bytes + sub * sub_bytes + row_off;
 #pragma unroll
-                for (uint32_t e = 0; e < 4; ++e)
-                    sts_v4(dst + (((c16 + e) ^ (r & 7u)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                for (uint32_t e = 0; e < 8; ++e)
+                    sts_v4(dst + ((e ^ (r & 7u)) << 4), o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1],
+                           o[e >> 2][4 * (e & 3) + 2], o[e >> 2][4 * (e & 3) + 3]);
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&a_full[s]));
-                if (++s == NS) { s = 0; ++round; }
+                if (lane == 0) mbar_arrive(smem_addr(&full[s]));
+                s += hop;
+                while (s >= NS) { s -= NS; ++round; }
             }
         }
     } else {
@@ -418,7 +522,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         uint32_t n = 0;
         for (uint32_t t = first; t < pl.tiles; t += step, ++n) {
             const uint32_t b = n & 1u;
-            bool ok = mbar_wait(smem_addr(&acc_full[b]), (n / 2) & 1u);
+            bool ok = mbar_wait_ring(smem_addr(&acc_full[b]), (n / 2) & 1u);
             ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -434,10 +538,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                         if (c0 + e < bt)
                             asm volatile("st.shared.b32 [%0], %1;" :: "r"(base + ((c0 + e) * 128u + il) * 4u), "r"(v[e]) : "memory");
                 } else if (i < a.ni) {
-#pragma unroll
-                    for (uint32_t e = 0; e < 32; ++e)
-                        if (c0 + e < cols)
-                            store_out(a, (size_t)(j0 + c0 + e) * a.ni + i, NV ? __fmul_rn(__uint_as_float(v[e]), sc) : __uint_as_float(v[e]));
+                    store_column(a, (size_t)(j0 + c0) * a.ni + i, min(32u, cols - c0), v, sc);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -490,6 +591,8 @@ cudaError_t x_map(const LinearArgs& a, uint32_t box_rows, CUtensorMap* map)
 
 uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
 
+uint32_t plan_stage_bytes(const MmaPlan& p) { return p.subs * (A_BYTES + p.bt * 128u); }
+
 // The tile width that takes the fewest rounds of tiles over the SMs, weighed by a round's
 // length (a stage costs bt, and no less than the 128 that widening its codes takes); then a
 // split of the contraction while tiles leave SMs idle and every part keeps four stages.
@@ -498,7 +601,6 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     MmaPlan p;
     const uint32_t unit = op == LIN_GRAD_WEIGHT ? 64u : 16u;
     p.tiles_i = ceil_div(a.ni, 128u);
-    p.kt = ceil_div(a.nc, 64u);
     const uint32_t most = std::min(256u, ceil_div(a.nj, unit) * unit);
     uint64_t best = ~0ull;
     p.bt = most;
@@ -508,16 +610,18 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
         if (cost < best) { best = cost; p.bt = bt; }
     }
     p.tiles = p.tiles_i * ceil_div(a.nj, p.bt);
+    p.subs = p.bt > 128u ? 1u : 2u;
+    p.kt = ceil_div(a.nc, 64u * p.subs);
     p.split = 1;
-    while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.kt >= p.split * 2 * 4) p.split *= 2;
-    p.stages = std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 1024u - 1024u) / (A_BYTES + p.bt * 128u));
+    while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.kt * p.subs >= p.split * 2 * 4) p.split *= 2;
+    p.stages = std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 2048u) / plan_stage_bytes(p));
     return p;
 }
 
 template <int OP, int FMT, bool NV>
 cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
 {
-    constexpr int P = Fmt<FMT>::four ? 4 : 2;
+    constexpr int P = Fmt<FMT>::four ? 2 : 1;
     constexpr auto kern = k_linear_mma<OP, FMT, NV, P>;
     static std::atomic<uint64_t> attr_set{0};        // a bit per device
     int dev = 0;
@@ -537,7 +641,7 @@ cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(pl.split > 1 ? pl.tiles * pl.split : std::min(pl.tiles, sms));
     cfg.blockDim = dim3(MMA_THREADS);
-    cfg.dynamicSmemBytes = pl.stages * (A_BYTES + pl.bt * 128u) + 1024u;
+    cfg.dynamicSmemBytes = pl.stages * plan_stage_bytes(pl) + 1024u;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -555,8 +659,8 @@ template <bool NV, int R>
 cudaError_t run_rows(const LinearArgs& a, cudaStream_t st)
 {
     const unsigned grid = ceil_div(a.ni, 16u * R);
-    return a.nj <= 8 ? launch_pdl(k_linear_rows<NV, R, 1>, grid, 32 * ROWS_WARPS, 0, st, a)
-                     : launch_pdl(k_linear_rows<NV, R, 2>, grid, 32 * ROWS_WARPS, 0, st, a);
+    return a.nj <= 8 ? launch_pdl(k_linear_rows<NV, R, 1, 2>, grid, 32 * ROWS_WARPS, 0, st, a)
+                     : launch_pdl(k_linear_rows<NV, R, 2, 1>, grid, 32 * ROWS_WARPS, 0, st, a);
 }
 
 template <bool NV>

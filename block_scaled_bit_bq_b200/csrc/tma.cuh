@@ -88,6 +88,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
+// mbar_wait for stage rings, whose waits are short and many: each try may sleep in hardware
+// until the phase completes (a hint of up to a millisecond) instead of polling, and the clock
+// is read only after tries have failed (reading it takes longer than most waits last).
+__device__ __forceinline__ bool mbar_wait_ring(uint32_t bar, uint32_t parity)
+{
+    for (int i = 0; i < 64; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
+        if (ok) return true;
+    }
+    return mbar_wait(bar, parity);
+}
+
 // 16-byte shared-memory accesses.
 __device__ __forceinline__ void lds_v4(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3)
 {
