@@ -240,9 +240,11 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 
 // ---------------------------------------------------------------------------
 // Tensor cores. out^T in tiles of 128 (i) x bt (j); 64 steps of the contraction per stage:
-//   A: Q widened to bf16, 128 i x 64 c (16 KB), written to shared memory by the widening warps:
-//      four groups of four warps take the stages in turn, a thread 64 codes of one stored row,
-//      which it fetched into registers P of its stages before;
+//   A: Q widened to bf16, 128 i x 64 c (16 KB), by the widening warps: four groups of four
+//      warps take the parts (64 steps) in turn, a thread 64 codes of one stored row. The codes
+//      come through a ring of their own, 16 KB chunks of four parts (two of 8-bit codes) by
+//      tensor-map copies, and what lies outside the matrix as zeros; the scales by plain loads,
+//      two of the thread's parts ahead;
 //   B: X by a tensor-map copy, bt j x 64 c.
 // Both with the 128-byte swizzle. Where the stored rows run along the contraction (LIN_FORWARD
 // for both operands, LIN_GRAD_INPUT for X) an operand is K-major: rows of 128 bytes, groups of
@@ -250,9 +252,9 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 // LIN_GRAD_WEIGHT) it is MN-major: chunks of 64 i (or j) x 64 c, a row of 128 bytes per c, and
 // the tensor cores transpose it. Either way a thread's 64 values are one row of 128 bytes.
 //
-// Warp 0 issues the copies, warp 1 the MMAs (4 of 16 steps a stage, fp32 accumulator in tensor
-// memory, two of them so that a tile's epilogue overlaps the next tile), warps 2-17 widen, warps
-// 18-21 write the accumulator out. A CTA per SM, persistent over the tiles; with fewer tiles
+// Warp 0 issues the copies of X, warp 22 those of the codes, warp 1 the MMAs (4 of 16 steps a
+// part, fp32 accumulator in tensor memory, two of them so that a tile's epilogue overlaps the
+// next tile), warps 2-17 widen, warps 18-21 write the accumulator out. A CTA per SM, persistent over the tiles; with fewer tiles
 // than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
 // through distributed shared memory, in rank order: no workspace, and the same sums every time.
 // Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
@@ -260,8 +262,10 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 
 constexpr uint32_t WIDEN_GROUPS = 4, GROUP_WARPS = 4, GROUP_THREADS = 32 * GROUP_WARPS;
 constexpr uint32_t WIDEN_WARPS = WIDEN_GROUPS * GROUP_WARPS;
-constexpr int MMA_THREADS = 32 * (2 + WIDEN_WARPS + 4);
-constexpr int MAX_STAGES = 8;
+constexpr uint32_t EPI_WARP = 2 + WIDEN_WARPS, CODES_WARP = EPI_WARP + 4;
+constexpr int MMA_THREADS = 32 * (CODES_WARP + 1);
+constexpr int MAX_STAGES = 8, MAX_CHUNKS = 8;
+constexpr uint32_t CHUNK_BYTES = 16384;
 constexpr uint32_t A_BYTES = 128u * 128u;
 constexpr uint32_t SMEM_MAX = 232448u;
 constexpr uint32_t ACC_COLS = 256;
@@ -270,6 +274,7 @@ struct MmaPlan {
     uint32_t bt;            // tile width in j: a multiple of 16 (of 64 for LIN_GRAD_WEIGHT), at most 256
     uint32_t subs;          // 64-step parts of a stage: 1 or 2
     uint32_t stages;        // of the ring
+    uint32_t chunks;        // of the code ring
     uint32_t tiles_i, tiles;
     uint32_t kt;            // stages of the contraction
     uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
@@ -323,19 +328,23 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     return v;
 }
 
-template <int OP, int FMT, bool NV, int P>
+template <int OP, int FMT, bool NV>
 __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_constant__ CUtensorMap xmap,
+                                                             const __grid_constant__ CUtensorMap qmap,
                                                              const LinearArgs a, const MmaPlan pl)
 {
     using W = Widen<FMT, NV>;
+    constexpr uint32_t CP = Fmt<FMT>::four ? 4u : 2u;     // parts of a chunk of codes
     extern __shared__ uint8_t linear_smem[];
-    __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], done_bar;
+    __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], code_full[MAX_CHUNKS],
+        code_empty[MAX_CHUNKS], acc_full[2], acc_empty[2], done_bar;
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t base = (smem_addr(linear_smem) + 1023u) & ~1023u;
     const uint32_t bt = pl.bt, subs = pl.subs, NS = pl.stages;
     const uint32_t b_bytes = bt * 128u, sub_bytes = A_BYTES + b_bytes, stage_bytes = subs * sub_bytes;
+    const uint32_t code_base = base + NS * stage_bytes;
     const uint32_t rank = pl.split > 1 ? cluster_rank() : 0u;
     // this CTA's tiles and its part of the contraction
     const uint32_t first = pl.split > 1 ? blockIdx.x / pl.split : blockIdx.x;
@@ -346,6 +355,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         for (uint32_t s = 0; s < NS; ++s) {
             mbar_init(smem_addr(&full[s]), subs * GROUP_WARPS + 1u);     // the widening warps, and the copies
             mbar_init(smem_addr(&empty[s]), 1);
+        }
+        for (uint32_t c = 0; c < pl.chunks; ++c) {
+            mbar_init(smem_addr(&code_full[c]), 1);
+            mbar_init(smem_addr(&code_empty[c]), CP * GROUP_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&acc_full[b]), 1);
@@ -364,6 +377,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_holder;
+    const uint32_t kts = (k1 - k0) * subs;           // parts of the contraction, a tile of this CTA
+    const uint32_t tile_chunks = (kts + CP - 1u) / CP;
     pdl_wait();
 
     if (warp == 0) {
@@ -442,68 +457,67 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     } else if (warp < 2 + WIDEN_WARPS) {
         // ---- Q tiles: a thread takes 64 codes of one stored row: forward, row r of the tile and
         // the part's columns; gradients, row r of the part and half h of the tile's columns.
-        // Group g takes parts g, g + 4, ... of this CTA's run of 64-step parts ----
-        const uint32_t grp_id = (warp - 2u) / GROUP_WARPS, tid = (threadIdx.x - 64u) % GROUP_THREADS;
+        // Group g takes parts g, g + 4, ... of a tile ----
+        const uint32_t g = (warp - 2u) / GROUP_WARPS, tid = (threadIdx.x - 64u) % GROUP_THREADS;
         const uint32_t r = OP == LIN_FORWARD ? tid : tid & 63u, h = OP == LIN_FORWARD ? 0u : tid >> 6;
-        const uint32_t row_off = h * 8192u + r * 128u;
-        const uint32_t row_bytes = Fmt<FMT>::four ? a.k / 2u : a.k;
-        constexpr uint32_t grp_bytes = Fmt<FMT>::four ? 16u : 32u;
-        const uint32_t groups = a.k / 32u, kts = (k1 - k0) * subs;   // parts of 64 steps per tile
+        // where its codes lie in a chunk: row cr of 128 (or 64) bytes, 16-byte units from cu on
+        const uint32_t cr = OP == LIN_FORWARD ? r : (g % CP) * 64u + r;
+        const uint32_t cu = OP == LIN_FORWARD ? 2u * g : (Fmt<FMT>::four ? 2u * h : 4u * h);
+        const uint32_t c_row = cr * (OP == LIN_GRAD_INPUT ? 64u : 128u), c_xor = OP == LIN_GRAD_INPUT ? (cr >> 1) & 3u : cr & 7u;
+        const uint32_t dst_off = (g % subs) * sub_bytes + h * 8192u + r * 128u;
+        const uint32_t groups = a.k / 32u;
         const bool wide = a.gemm_layout || (NV ? a.nb % 4u == 0 : a.nb % 2u == 0);
-        uint32_t ld_tile = first, ld_kk = grp_id;            // the next part to fetch
-        uint32_t w[P][2][W::WORDS], sc[P][2];
-        auto fetch = [&](uint32_t (&cw)[2][W::WORDS], uint32_t (&cs)[2]) {
-            while (ld_kk >= kts && ld_tile < pl.tiles) { ld_kk -= kts; ld_tile += step; }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                cs[x] = 0u;
-#pragma unroll
-                for (int e = 0; e < W::WORDS; ++e) cw[x][e] = 0u;
-            }
-            if (ld_tile < pl.tiles) {
-                const uint32_t i0 = ld_tile % pl.tiles_i * 128u, kk = k0 * subs + ld_kk;
+        constexpr int P = 2;
+        uint32_t ld_tile = first, ld_pk = g, sc[P][2];        // the next part whose scales are to be loaded
+        auto fetch = [&](uint32_t (&cs)[2]) {
+            cs[0] = cs[1] = 0u;
+            if (ld_pk >= kts) { ld_pk = g; ld_tile += step; }
+            if (ld_tile < pl.tiles && ld_pk < kts) {
+                const uint32_t i0 = ld_tile % pl.tiles_i * 128u, kk = k0 * subs + ld_pk;
                 const uint32_t row = OP == LIN_FORWARD ? i0 + r : kk * 64u + r;
                 const uint32_t grp = OP == LIN_FORWARD ? kk * 2u : i0 / 32u + 2u * h;
-                if (row < a.q_rows && grp < groups) {
-                    const uint8_t* p = a.codes + (size_t)row * row_bytes + (size_t)grp * grp_bytes;
-                    const bool second = grp + 1u < groups;
-                    if constexpr (W::WORDS == 4) {
-                        ld_nc_v4(p, cw[0]);
-                        if (second) ld_nc_v4(p + 16, cw[1]);
-                    } else {
-                        ld_nc_v8(p, cw[0]);
-                        if (second) ld_nc_v8(p + 32, cw[1]);
-                    }
-                    load_scale_pair<NV>(a, row, grp, wide, second, cs);
-                }
+                if (row < a.q_rows && grp < groups) load_scale_pair<NV>(a, row, grp, wide, grp + 1u < groups, cs);
             }
-            ld_kk += WIDEN_GROUPS;
+            ld_pk += WIDEN_GROUPS;
         };
 #pragma unroll
-        for (int p = 0; p < P; ++p) fetch(w[p], sc[p]);
-        const uint32_t my_tiles = (pl.tiles - first + step - 1u) / step;
-        const uint64_t total = (uint64_t)my_tiles * kts;
-        uint32_t s = grp_id / subs, round = 0;               // NS * subs >= 4: no group starts past the ring
-        const uint32_t sub = grp_id % subs, hop = WIDEN_GROUPS / subs;
+        for (int p = 0; p < P; ++p) fetch(sc[p]);
+        uint32_t odd = 0;                            // which scales are next
+        uint32_t part0 = 0, chunk0 = 0;              // parts and chunks of the tiles before
         bool ok = true;
-        for (uint64_t it = grp_id; it < total && ok; it += P * WIDEN_GROUPS) {
+        for (uint32_t t = first; t < pl.tiles && ok; t += step, part0 += kts, chunk0 += tile_chunks) {
+            uint32_t s = (part0 + g) / subs, round = s / NS;      // slot of the stage ring
+            s -= round * NS;
+            uint32_t c = chunk0 + g / CP, c_par = c / pl.chunks;  // slot of the code ring
+            c -= c_par * pl.chunks;
+            c_par &= 1u;
+            uint32_t pk = g;
+            for (; pk < kts && ok; pk += WIDEN_GROUPS) {
+                ok = mbar_wait_ring(smem_addr(&code_full[c]), c_par);
+                const uint32_t src = code_base + c * CHUNK_BYTES + c_row;
+                uint32_t o[2][16], w[2][W::WORDS];
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                if (it + p * WIDEN_GROUPS >= total || !ok) continue;
-                uint32_t o[2][16];
+                for (uint32_t x = 0; x < 2; ++x)
+#pragma unroll
+                    for (uint32_t e = 0; e < W::WORDS / 4; ++e)
+                        lds_v4(src + (((cu + x * (W::WORDS / 4) + e) ^ c_xor) << 4), w[x][4 * e], w[x][4 * e + 1],
+                               w[x][4 * e + 2], w[x][4 * e + 3]);
+                const uint32_t s0 = odd ? sc[1][0] : sc[0][0], s1 = odd ? sc[1][1] : sc[0][1];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t v[W::WORDS * W::RAW];
-                    W::pairs(w[p][x], sc[p][x], v);
+                    W::pairs(w[x], x ? s1 : s0, v);
                     W::in_order(v, o[x]);
                 }
-                fetch(w[p], sc[p]);
-                if (round > 0) {
-                    ok = mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u);
-                    ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
-                    if (!ok) { abort_flag = 1; continue; }
-                }
-                const uint32_t dst = base + s * stage_bytes + sub * sub_bytes + row_off;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&code_empty[c]));
+                if (odd) fetch(sc[1]);
+                else fetch(sc[0]);
+                odd ^= 1u;
+                if (ok && round > 0) ok = mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u);
+                ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
+                if (!ok) { abort_flag = 1; break; }
+                const uint32_t dst = base + s * stage_bytes + dst_off;
 #pragma unroll
                 for (uint32_t e = 0; e < 8; ++e)
                     sts_v4(dst + ((e ^ (r & 7u)) << 4), o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1],
@@ -511,9 +525,44 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&full[s]));
-                s += hop;
+                s += WIDEN_GROUPS / subs;
                 while (s >= NS) { s -= NS; ++round; }
+                c += WIDEN_GROUPS / CP;
+                while (c >= pl.chunks) { c -= pl.chunks; c_par ^= 1u; }
             }
+            // a tile's last chunk may lack this group's part: it is released all the same (once it
+            // has arrived, so that the arrival counts for this use of the slot)
+            if (ok && pk / CP < tile_chunks) {
+                ok = mbar_wait_ring(smem_addr(&code_full[c]), c_par);
+                ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
+                if (!ok) abort_flag = 1;
+                else if (lane == 0) mbar_arrive(smem_addr(&code_empty[c]));
+            }
+        }
+    } else if (warp == CODES_WARP) {
+        // ---- codes: forward, boxes of 128 rows x 256 columns along the tile's rows; gradients,
+        // boxes of 256 (128) rows of the contraction x the tile's 128 columns ----
+        const bool leader = elect_one();
+        uint32_t c = 0, round = 0;
+        for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+            const uint32_t i0 = t % pl.tiles_i * 128u;
+            for (uint32_t n = 0; n < tile_chunks; ++n) {
+                if (round > 0 && !mbar_wait_ring(smem_addr(&code_empty[c]), (round - 1) & 1u)) { abort_flag = 1; break; }
+                if (abort_flag) break;
+                if (leader) {
+                    const uint32_t part = k0 * subs + n * CP, fb = smem_addr(&code_full[c]);
+                    mbar_arrive_expect_tx(fb, CHUNK_BYTES);
+                    if (OP == LIN_FORWARD) tma_load_2d(code_base + c * CHUNK_BYTES, &qmap, fb, (int)(part * 32u), (int)i0);
+                    else tma_load_2d(code_base + c * CHUNK_BYTES, &qmap, fb, (int)(Fmt<FMT>::four ? i0 / 2u : i0), (int)(part * 64u));
+                }
+                __syncwarp();
+                if (++c == pl.chunks) { c = 0; ++round; }
+            }
+        }
+        if (abort_flag) {
+            // let the copies in flight land before the CTA can exit (bounded)
+            for (uint32_t j = 0; j < pl.chunks && (round > 0 || j < c); ++j)
+                (void)mbar_wait(smem_addr(&code_full[j]), (j < c ? round : round - 1) & 1u);
         }
     } else {
         // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, i.e. 32 i ----
@@ -572,6 +621,24 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     }
 }
 
+// The codes as stored: boxes of CHUNK_BYTES (see the codes warp).
+cudaError_t codes_map(int op, bool four, const LinearArgs& a, CUtensorMap* map)
+{
+    *map = CUtensorMap{};
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const uint32_t row_bytes = four ? a.k / 2u : a.k, width = op == LIN_GRAD_INPUT ? 64u : 128u;
+    const cuuint64_t dims[2] = {row_bytes, a.q_rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {width, CHUNK_BYTES / width};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.codes), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           op == LIN_GRAD_INPUT ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // x as stored, boxes of 64 columns (128 bytes) x box_rows rows, 128-byte swizzle; what lies
 // outside the matrix arrives as zeros.
 cudaError_t x_map(const LinearArgs& a, uint32_t box_rows, CUtensorMap* map)
@@ -614,15 +681,18 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     p.kt = ceil_div(a.nc, 64u * p.subs);
     p.split = 1;
     while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.kt * p.subs >= p.split * 2 * 4) p.split *= 2;
-    p.stages = std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 2048u) / plan_stage_bytes(p));
+    // two chunks of codes at least, up to four stages, then more chunks: with narrow tiles the
+    // codes are most of what is read, and their ring keeps the memory busy
+    const uint32_t room = SMEM_MAX - 2048u, stage = plan_stage_bytes(p);
+    p.stages = std::min(4u, (room - 2u * CHUNK_BYTES) / stage);
+    p.chunks = std::min<uint32_t>(MAX_CHUNKS, (room - p.stages * stage) / CHUNK_BYTES);
     return p;
 }
 
 template <int OP, int FMT, bool NV>
 cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
 {
-    constexpr int P = Fmt<FMT>::four ? 2 : 1;
-    constexpr auto kern = k_linear_mma<OP, FMT, NV, P>;
+    constexpr auto kern = k_linear_mma<OP, FMT, NV>;
     static std::atomic<uint64_t> attr_set{0};        // a bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -635,13 +705,15 @@ cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
     }
     const uint32_t sms = (uint32_t)device_sm_count();
     const MmaPlan pl = make_mma_plan(OP, a, sms);
-    CUtensorMap xm;
+    CUtensorMap xm, qm;
     e = x_map(a, OP == LIN_GRAD_WEIGHT ? 64u : pl.bt, &xm);
+    if (e != cudaSuccess) return e;
+    e = codes_map(OP, Fmt<FMT>::four, a, &qm);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(pl.split > 1 ? pl.tiles * pl.split : std::min(pl.tiles, sms));
     cfg.blockDim = dim3(MMA_THREADS);
-    cfg.dynamicSmemBytes = pl.stages * plan_stage_bytes(pl) + 1024u;
+    cfg.dynamicSmemBytes = pl.stages * plan_stage_bytes(pl) + pl.chunks * CHUNK_BYTES + 1024u;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -652,7 +724,7 @@ cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = pl.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, xm, a, pl);
+    return cudaLaunchKernelEx(&cfg, kern, xm, qm, a, pl);
 }
 
 template <bool NV, int R>
