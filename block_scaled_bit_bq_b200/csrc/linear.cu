@@ -66,20 +66,26 @@ __device__ __forceinline__ uint32_t load_scale(const LinearArgs& a, uint32_t row
 }
 
 // The same of two 32-code groups, grp (even) and grp + 1, the second where it exists: in one
-// load where a row's scales start on a multiple of its size (wide).
+// load where a row's scales start on a multiple of its size (wide). The loaded words are taken
+// apart only where they are used (pair_scale): doing so here would wait for them.
 template <bool NV>
 __device__ __forceinline__ void load_scale_pair(const LinearArgs& a, uint32_t row, uint32_t grp, bool wide, bool second,
                                                 uint32_t (&s)[2])
 {
     const uint8_t* p = a.scales + scale_offset(a, row, NV ? 2 * grp : grp);
     if (wide) {
-        const uint32_t v = NV ? ldg_u32(p) : ldg_u16(p);
-        s[0] = NV ? v & 0xFFFFu : v & 0xFFu;
-        s[1] = NV ? v >> 16 : v >> 8;
+        s[0] = NV ? ldg_u32(p) : ldg_u16(p);
     } else {
         s[0] = NV ? ldg_u16(p) : ldg_u8(p);
         if (second) s[1] = NV ? ldg_u16(p + 2) : ldg_u8(p + 1);
     }
+}
+
+template <bool NV>
+__device__ __forceinline__ uint32_t pair_scale(const uint32_t (&s)[2], bool wide, int which)
+{
+    if (which == 0) return NV ? s[0] & 0xFFFFu : s[0] & 0xFFu;
+    return wide ? (NV ? s[0] >> 16 : s[0] >> 8) : s[1];
 }
 
 template <bool NV>
@@ -269,6 +275,8 @@ constexpr uint32_t CHUNK_BYTES = 16384;
 constexpr uint32_t A_BYTES = 128u * 128u;
 constexpr uint32_t SMEM_MAX = 232448u;
 constexpr uint32_t ACC_COLS = 256;
+constexpr uint32_t SMEM_ROOM = SMEM_MAX - 2048u;       // less alignment slack and static shared memory
+static_assert(SMEM_ROOM - 2u * CHUNK_BYTES >= WIDEN_GROUPS * (A_BYTES + 256u * 128u), "a stage ring of as many parts as groups");
 
 struct MmaPlan {
     uint32_t bt;            // tile width in j: a multiple of 16 (of 64 for LIN_GRAD_WEIGHT), at most 256
@@ -468,25 +476,31 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint32_t groups = a.k / 32u;
         const bool wide = a.gemm_layout || (NV ? a.nb % 4u == 0 : a.nb % 2u == 0);
         constexpr int P = 2;
-        uint32_t ld_tile = first, ld_pk = g, sc[P][2];        // the next part whose scales are to be loaded
+        uint32_t ld_tile = first, ld_pk = g, ld_i0 = first % pl.tiles_i * 128u;    // the next part whose
+        uint32_t sc[P][2];                                                           // scales are to be loaded
         auto fetch = [&](uint32_t (&cs)[2]) {
             cs[0] = cs[1] = 0u;
-            if (ld_pk >= kts) { ld_pk = g; ld_tile += step; }
+            if (ld_pk >= kts) {
+                ld_pk = g;
+                ld_tile += step;
+                ld_i0 = ld_tile % pl.tiles_i * 128u;
+            }
             if (ld_tile < pl.tiles && ld_pk < kts) {
-                const uint32_t i0 = ld_tile % pl.tiles_i * 128u, kk = k0 * subs + ld_pk;
-                const uint32_t row = OP == LIN_FORWARD ? i0 + r : kk * 64u + r;
-                const uint32_t grp = OP == LIN_FORWARD ? kk * 2u : i0 / 32u + 2u * h;
+                const uint32_t kk = k0 * subs + ld_pk;
+                const uint32_t row = OP == LIN_FORWARD ? ld_i0 + r : kk * 64u + r;
+                const uint32_t grp = OP == LIN_FORWARD ? kk * 2u : ld_i0 / 32u + 2u * h;
                 if (row < a.q_rows && grp < groups) load_scale_pair<NV>(a, row, grp, wide, grp + 1u < groups, cs);
             }
             ld_pk += WIDEN_GROUPS;
         };
 #pragma unroll
         for (int p = 0; p < P; ++p) fetch(sc[p]);
-        uint32_t odd = 0;                            // which scales are next
         uint32_t part0 = 0, chunk0 = 0;              // parts and chunks of the tiles before
         bool ok = true;
         for (uint32_t t = first; t < pl.tiles && ok; t += step, part0 += kts, chunk0 += tile_chunks) {
-            uint32_t s = (part0 + g) / subs, round = s / NS;      // slot of the stage ring
+            // slot of the stage ring. The ring holds at least as many parts as there are groups: a
+            // wait by parity then never looks back further than one use of its slot
+            uint32_t s = (part0 + g) / subs, round = s / NS;
             s -= round * NS;
             uint32_t c = chunk0 + g / CP, c_par = c / pl.chunks;  // slot of the code ring
             c -= c_par * pl.chunks;
@@ -502,7 +516,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                     for (uint32_t e = 0; e < W::WORDS / 4; ++e)
                         lds_v4(src + (((cu + x * (W::WORDS / 4) + e) ^ c_xor) << 4), w[x][4 * e], w[x][4 * e + 1],
                                w[x][4 * e + 2], w[x][4 * e + 3]);
-                const uint32_t s0 = odd ? sc[1][0] : sc[0][0], s1 = odd ? sc[1][1] : sc[0][1];
+                const uint32_t s0 = pair_scale<NV>(sc[0], wide, 0), s1 = pair_scale<NV>(sc[0], wide, 1);
+                sc[0][0] = sc[1][0];
+                sc[0][1] = sc[1][1];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t v[W::WORDS * W::RAW];
@@ -511,9 +527,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&code_empty[c]));
-                if (odd) fetch(sc[1]);
-                else fetch(sc[0]);
-                odd ^= 1u;
+                fetch(sc[1]);
                 if (ok && round > 0) ok = mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u);
                 ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
                 if (!ok) { abort_flag = 1; break; }
@@ -683,8 +697,8 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.kt * p.subs >= p.split * 2 * 4) p.split *= 2;
     // two chunks of codes at least, up to four stages, then more chunks: with narrow tiles the
     // codes are most of what is read, and their ring keeps the memory busy
-    const uint32_t room = SMEM_MAX - 2048u, stage = plan_stage_bytes(p);
-    p.stages = std::min(4u, (room - 2u * CHUNK_BYTES) / stage);
+    const uint32_t room = SMEM_ROOM, stage = plan_stage_bytes(p);
+    p.stages = std::min(4u, (room - 2u * CHUNK_BYTES) / stage);          // times subs >= 4 parts (see there)
     p.chunks = std::min<uint32_t>(MAX_CHUNKS, (room - p.stages * stage) / CHUNK_BYTES);
     return p;
 }
