@@ -260,7 +260,10 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 //
 // Warp 0 issues the copies of X, warp 22 those of the codes, warp 1 the MMAs (4 of 16 steps a
 // part, fp32 accumulator in tensor memory, two of them so that a tile's epilogue overlaps the
-// next tile), warps 2-17 widen, warps 18-21 write the accumulator out. A CTA per SM, persistent over the tiles; with fewer tiles
+// next tile), warps 2-17 widen, warps 18-21 write the accumulator out. A CTA per SM, persistent
+// over the tiles. Large products run on pairs of CTAs (PAIR): a tile is 256 i x 256 j, each CTA
+// of a pair widens its own 128 i and copies its own 128 j, and the first one issues MMAs that
+// read both (half the shared memory and copies of X per MMA of a lone CTA). With fewer tiles
 // than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
 // through distributed shared memory, in rank order: no workspace, and the same sums every time.
 // Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
@@ -284,27 +287,67 @@ struct MmaPlan {
     uint32_t stages;        // of the ring
     uint32_t chunks;        // of the code ring
     uint32_t tiles_i, tiles;
-    uint32_t kt;            // stages of the contraction
+    uint32_t blocks;        // of the contraction: 256 steps, four parts, each
     uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
+    uint32_t pair;          // 1: tiles of 256 x 256 on pairs of CTAs (bt 128 each)
 };
 
 // Instruction descriptor of the bf16 MMA: fp32 accumulator (bits 4-5), bf16 operands (7-9,
 // 10-12), MN-major flags of A and B (15, 16), N / 8 (17-22), M / 16 (24-28).
 template <int OP>
-__device__ __forceinline__ uint32_t mma_desc(uint32_t bt)
+__device__ __forceinline__ uint32_t mma_desc(uint32_t m, uint32_t n)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((OP == LIN_FORWARD ? 0u : 1u) << 15) |
-           ((OP == LIN_GRAD_WEIGHT ? 1u : 0u) << 16) | ((bt >> 3) << 17) | ((128u >> 4) << 24);
+           ((OP == LIN_GRAD_WEIGHT ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 // MN-major operand: chunks of 64 x 64 (8 KB) side by side, 8 steps 1024 bytes apart.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) { return smem_desc(addr, 8192u, 1024u, 2u); }
 
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    if constexpr (PAIR)
+        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    else
+        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Commit of the MMAs so far: an arrival on bar, in a pair on that barrier of both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_all(uint32_t bar)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     :: "r"(bar), "h"((uint16_t)3) : "memory");
+    else
+        tc_commit(bar);
+}
+
+// Arrival on the first CTA's barrier (bar: its address in this CTA), and a wait that sees what
+// came before such arrivals.
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
+{
+    asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %0, 0;\n"
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [p];\n}" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i) {
+            uint32_t ok;
+            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+                         " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
+            if (ok) return true;
+        }
+        if (global_ns() - t0 > WAIT_LIMIT_NS) return false;
+    }
 }
 
 // One lane of a converged warp.
@@ -336,7 +379,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     return v;
 }
 
-template <int OP, int FMT, bool NV>
+template <int OP, int FMT, bool NV, bool PAIR>
 __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_constant__ CUtensorMap xmap,
                                                              const __grid_constant__ CUtensorMap qmap,
                                                              const LinearArgs a, const MmaPlan pl)
@@ -350,18 +393,30 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     __shared__ volatile int abort_flag;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t base = (smem_addr(linear_smem) + 1023u) & ~1023u;
+    // bt: the j that this CTA copies; a pair's tile has twice as many
     const uint32_t bt = pl.bt, subs = pl.subs, NS = pl.stages;
+    const uint32_t tile_j = PAIR ? 2u * bt : bt;
     const uint32_t b_bytes = bt * 128u, sub_bytes = A_BYTES + b_bytes, stage_bytes = subs * sub_bytes;
     const uint32_t code_base = base + NS * stage_bytes;
-    const uint32_t rank = pl.split > 1 ? cluster_rank() : 0u;
-    // this CTA's tiles and its part of the contraction
-    const uint32_t first = pl.split > 1 ? blockIdx.x / pl.split : blockIdx.x;
-    const uint32_t step = pl.split > 1 ? pl.tiles : gridDim.x;
-    const uint32_t k0 = (uint32_t)((uint64_t)pl.kt * rank / pl.split), k1 = (uint32_t)((uint64_t)pl.kt * (rank + 1) / pl.split);
+    const uint32_t rank = PAIR || pl.split > 1 ? cluster_rank() : 0u;
+    // this CTA's (pair's) tiles and its part of the contraction
+    const uint32_t share = PAIR ? 2u : pl.split;
+    const uint32_t first = share > 1 ? blockIdx.x / share : blockIdx.x;
+    const uint32_t step = PAIR ? gridDim.x / 2u : pl.split > 1 ? pl.tiles : gridDim.x;
+    const uint32_t krank = PAIR ? 0u : rank;
+    const uint32_t p0 = 4u * (uint32_t)((uint64_t)pl.blocks * krank / pl.split);          // first part
+    const uint32_t kts = 4u * (uint32_t)((uint64_t)pl.blocks * (krank + 1) / pl.split) - p0;   // parts
+    const uint32_t tile_stages = kts / subs, tile_chunks = kts / CP;
+    // parts past the contraction's end fill up its last block: they take part in every hand-over,
+    // but nothing is copied, widened or multiplied for them
+    auto live = [&](uint32_t part) { return (uint64_t)part * 64u < a.nc; };
+    // first i of a tile for this CTA
+    auto tile_i0 = [&](uint32_t t) { return t % pl.tiles_i * (PAIR ? 256u : 128u) + (PAIR ? rank * 128u : 0u); };
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < NS; ++s) {
-            mbar_init(smem_addr(&full[s]), subs * GROUP_WARPS + 1u);     // the widening warps, and the copies
+            // the widening warps, the copies, and the other CTA of the pair
+            mbar_init(smem_addr(&full[s]), subs * GROUP_WARPS + 1u + (PAIR && rank == 0 ? 1u : 0u));
             mbar_init(smem_addr(&empty[s]), 1);
         }
         for (uint32_t c = 0; c < pl.chunks; ++c) {
@@ -370,23 +425,30 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&acc_full[b]), 1);
-            mbar_init(smem_addr(&acc_empty[b]), 4);
+            mbar_init(smem_addr(&acc_empty[b]), PAIR ? 8 : 4);
         }
         mbar_init(smem_addr(&done_bar), 1);
         abort_flag = 0;
         fence_mbar_init();
     }
+    __syncwarp();
+    if (PAIR) cluster_sync();                        // the other CTA is there, its barriers are set
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     :: "r"(smem_addr(&tmem_holder)), "r"(2u * ACC_COLS) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         :: "r"(smem_addr(&tmem_holder)), "r"(2u * ACC_COLS) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         :: "r"(smem_addr(&tmem_holder)), "r"(2u * ACC_COLS) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    if (PAIR) cluster_sync();                        // the first CTA's MMAs use both accumulators
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_holder;
-    const uint32_t kts = (k1 - k0) * subs;           // parts of the contraction, a tile of this CTA
-    const uint32_t tile_chunks = (kts + CP - 1u) / CP;
     pdl_wait();
 
     if (warp == 0) {
@@ -394,16 +456,17 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const bool leader = elect_one();
         uint32_t s = 0, round = 0;                   // slot of the ring, and how often it wrapped
         for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
-            const int j0 = (int)(t / pl.tiles_i * bt);
-            for (uint32_t kk = k0; kk < k1; ++kk) {
+            const int j0 = (int)(t / pl.tiles_i * tile_j + (PAIR ? rank * bt : 0u));
+            for (uint32_t kk = 0; kk < tile_stages; ++kk) {
                 if (round > 0 && !mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u)) { abort_flag = 1; break; }
                 if (abort_flag) break;
                 if (leader) {
                     const uint32_t fb = smem_addr(&full[s]);
-                    uint32_t dst = base + s * stage_bytes + A_BYTES;
-                    mbar_arrive_expect_tx(fb, subs * b_bytes);
-                    for (uint32_t u = 0; u < subs; ++u, dst += sub_bytes) {
-                        const int c = (int)((kk * subs + u) * 64u);
+                    uint32_t dst = base + s * stage_bytes + A_BYTES, part = p0 + kk * subs;
+                    const uint32_t n_live = live(part) ? (subs == 2 && live(part + 1) ? 2u : 1u) : 0u;
+                    mbar_arrive_expect_tx(fb, n_live * b_bytes);
+                    for (uint32_t u = 0; u < n_live; ++u, ++part, dst += sub_bytes) {
+                        const int c = (int)(part * 64u);
                         if (OP == LIN_GRAD_WEIGHT) {
                             for (uint32_t x = 0; x < bt / 64u; ++x)
                                 tma_load_2d(dst + x * 8192u, &xmap, fb, j0 + (int)(64u * x), c);
@@ -428,44 +491,62 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         // chunk. The whole warp runs the loop, so that descriptors stay in uniform registers ----
         constexpr uint32_t ka = OP == LIN_FORWARD ? 2u : 128u, kb = OP == LIN_GRAD_WEIGHT ? 128u : 2u;
         const bool leader = elect_one();
-        const uint32_t idesc = mma_desc<OP>(bt);
+        const uint32_t idesc = mma_desc<OP>(PAIR ? 256u : 128u, tile_j);
         const uint64_t ad0 = OP == LIN_FORWARD ? operand_desc(base) : mn_desc(base);
         const uint64_t bd0 = OP == LIN_GRAD_WEIGHT ? mn_desc(base + A_BYTES) : operand_desc(base + A_BYTES);
+        auto wait = [](uint32_t bar, uint32_t parity) { return PAIR ? mbar_wait_pair(bar, parity) : mbar_wait_ring(bar, parity); };
         uint32_t s = 0, par = 0, i = 0;
-        for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
-            const uint32_t b = i & 1u;
-            if (i >= 2 && !mbar_wait_ring(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t d = tmem + b * ACC_COLS;
-            uint32_t acc = 0;
-            for (uint32_t kk = k0; kk < k1; ++kk) {
-                if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
-                if (abort_flag) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (uint32_t u = 0; u < subs; ++u) {
-                    const uint64_t so = (s * stage_bytes + u * sub_bytes) >> 4, ad = ad0 + so, bd = bd0 + so;
-                    if (leader) {
-#pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k) tc_mma_bf16(d, ad + ka * k, bd + kb * k, idesc, k ? 1u : acc);
-                    }
-                    acc = 1;
+        if (PAIR && rank != 0) {
+            // the second CTA of a pair only says when its half of a stage is there
+            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+                for (uint32_t kk = 0; kk < tile_stages; ++kk) {
+                    if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
+                    if (abort_flag) break;
+                    if (leader) mbar_arrive_first(smem_addr(&full[s]));
+                    __syncwarp();
+                    if (++s == NS) { s = 0; par ^= 1u; }
                 }
-                if (leader) tc_commit(smem_addr(&empty[s]));
-                __syncwarp();
-                if (++s == NS) { s = 0; par ^= 1u; }
             }
-            if (abort_flag) break;
-            if (leader) tc_commit(smem_addr(&acc_full[b]));
+        } else {
+            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
+                const uint32_t b = i & 1u;
+                if (i >= 2 && !wait(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + b * ACC_COLS;
+                uint32_t acc = 0;
+                for (uint32_t kk = 0; kk < tile_stages; ++kk) {
+                    if (!wait(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
+                    if (abort_flag) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    for (uint32_t u = 0; u < subs; ++u) {
+                        const uint64_t so = (s * stage_bytes + u * sub_bytes) >> 4, ad = ad0 + so, bd = bd0 + so;
+                        if (leader && live(p0 + kk * subs + u)) {
+#pragma unroll
+                            for (uint32_t k = 0; k < 4; ++k)
+                                tc_mma_bf16<PAIR>(d, ad + ka * k, bd + kb * k, idesc, k ? 1u : acc);
+                        }
+                        acc = 1;
+                    }
+                    if (leader) tc_commit_all<PAIR>(smem_addr(&empty[s]));
+                    __syncwarp();
+                    if (++s == NS) { s = 0; par ^= 1u; }
+                }
+                if (abort_flag) break;
+                if (leader) tc_commit_all<PAIR>(smem_addr(&acc_full[b]));
+                __syncwarp();
+            }
+            // every MMA issued so far completes before done_bar's phase does
+            if (leader) tc_commit_all<PAIR>(smem_addr(&done_bar));
             __syncwarp();
         }
-        // every MMA issued so far completes before done_bar's phase does
-        if (leader) tc_commit(smem_addr(&done_bar));
-        __syncwarp();
         if (!mbar_wait(smem_addr(&done_bar), 0u)) abort_flag = 1;
     } else if (warp < 2 + WIDEN_WARPS) {
         // ---- Q tiles: a thread takes 64 codes of one stored row: forward, row r of the tile and
         // the part's columns; gradients, row r of the part and half h of the tile's columns.
-        // Group g takes parts g, g + 4, ... of a tile ----
+        // Group g takes parts g, g + 4, ... (a tile has a multiple of four): it comes by every fourth
+        // part of the stage ring and every chunk of codes (of 8-bit codes, every second), so its
+        // waits by parity never look back further than one use of a slot: the stage ring holds four
+        // parts or more, the code ring two chunks or more (of 8-bit codes, an even number) ----
         const uint32_t g = (warp - 2u) / GROUP_WARPS, tid = (threadIdx.x - 64u) % GROUP_THREADS;
         const uint32_t r = OP == LIN_FORWARD ? tid : tid & 63u, h = OP == LIN_FORWARD ? 0u : tid >> 6;
         // where its codes lie in a chunk: row cr of 128 (or 64) bytes, 16-byte units from cu on
@@ -476,17 +557,17 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint32_t groups = a.k / 32u;
         const bool wide = a.gemm_layout || (NV ? a.nb % 4u == 0 : a.nb % 2u == 0);
         constexpr int P = 2;
-        uint32_t ld_tile = first, ld_pk = g, ld_i0 = first % pl.tiles_i * 128u;    // the next part whose
-        uint32_t sc[P][2];                                                           // scales are to be loaded
+        uint32_t ld_tile = first, ld_pk = g, ld_i0 = tile_i0(first);   // the next part whose scales
+        uint32_t sc[P][2];                                           // are to be loaded
         auto fetch = [&](uint32_t (&cs)[2]) {
             cs[0] = cs[1] = 0u;
             if (ld_pk >= kts) {
                 ld_pk = g;
                 ld_tile += step;
-                ld_i0 = ld_tile % pl.tiles_i * 128u;
+                ld_i0 = tile_i0(ld_tile);
             }
             if (ld_tile < pl.tiles && ld_pk < kts) {
-                const uint32_t kk = k0 * subs + ld_pk;
+                const uint32_t kk = p0 + ld_pk;
                 const uint32_t row = OP == LIN_FORWARD ? ld_i0 + r : kk * 64u + r;
                 const uint32_t grp = OP == LIN_FORWARD ? kk * 2u : ld_i0 / 32u + 2u * h;
                 if (row < a.q_rows && grp < groups) load_scale_pair<NV>(a, row, grp, wide, grp + 1u < groups, cs);
@@ -495,18 +576,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         };
 #pragma unroll
         for (int p = 0; p < P; ++p) fetch(sc[p]);
-        uint32_t part0 = 0, chunk0 = 0;              // parts and chunks of the tiles before
+        uint32_t s = g / subs, round = 0, c = g / CP, c_par = 0;      // slots of the two rings
         bool ok = true;
-        for (uint32_t t = first; t < pl.tiles && ok; t += step, part0 += kts, chunk0 += tile_chunks) {
-            // slot of the stage ring. The ring holds at least as many parts as there are groups: a
-            // wait by parity then never looks back further than one use of its slot
-            uint32_t s = (part0 + g) / subs, round = s / NS;
-            s -= round * NS;
-            uint32_t c = chunk0 + g / CP, c_par = c / pl.chunks;  // slot of the code ring
-            c -= c_par * pl.chunks;
-            c_par &= 1u;
-            uint32_t pk = g;
-            for (; pk < kts && ok; pk += WIDEN_GROUPS) {
+        for (uint32_t t = first; t < pl.tiles && ok; t += step) {
+            for (uint32_t pk = g; pk < kts && ok; pk += WIDEN_GROUPS) {
                 ok = mbar_wait_ring(smem_addr(&code_full[c]), c_par);
                 const uint32_t src = code_base + c * CHUNK_BYTES + c_row;
                 uint32_t o[2][16], w[2][W::WORDS];
@@ -531,26 +604,20 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 if (ok && round > 0) ok = mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u);
                 ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
                 if (!ok) { abort_flag = 1; break; }
-                const uint32_t dst = base + s * stage_bytes + dst_off;
+                if (live(p0 + pk)) {
+                    const uint32_t dst = base + s * stage_bytes + dst_off;
 #pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    sts_v4(dst + ((e ^ (r & 7u)) << 4), o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1],
-                           o[e >> 2][4 * (e & 3) + 2], o[e >> 2][4 * (e & 3) + 3]);
-                fence_proxy_async();
+                    for (uint32_t e = 0; e < 8; ++e)
+                        sts_v4(dst + ((e ^ (r & 7u)) << 4), o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1],
+                               o[e >> 2][4 * (e & 3) + 2], o[e >> 2][4 * (e & 3) + 3]);
+                    fence_proxy_async();
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&full[s]));
                 s += WIDEN_GROUPS / subs;
                 while (s >= NS) { s -= NS; ++round; }
                 c += WIDEN_GROUPS / CP;
                 while (c >= pl.chunks) { c -= pl.chunks; c_par ^= 1u; }
-            }
-            // a tile's last chunk may lack this group's part: it is released all the same (once it
-            // has arrived, so that the arrival counts for this use of the slot)
-            if (ok && pk / CP < tile_chunks) {
-                ok = mbar_wait_ring(smem_addr(&code_full[c]), c_par);
-                ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
-                if (!ok) abort_flag = 1;
-                else if (lane == 0) mbar_arrive(smem_addr(&code_empty[c]));
             }
         }
     } else if (warp == CODES_WARP) {
@@ -559,12 +626,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const bool leader = elect_one();
         uint32_t c = 0, round = 0;
         for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
-            const uint32_t i0 = t % pl.tiles_i * 128u;
+            const uint32_t i0 = tile_i0(t);
             for (uint32_t n = 0; n < tile_chunks; ++n) {
                 if (round > 0 && !mbar_wait_ring(smem_addr(&code_empty[c]), (round - 1) & 1u)) { abort_flag = 1; break; }
                 if (abort_flag) break;
                 if (leader) {
-                    const uint32_t part = k0 * subs + n * CP, fb = smem_addr(&code_full[c]);
+                    const uint32_t part = p0 + n * CP, fb = smem_addr(&code_full[c]);
                     mbar_arrive_expect_tx(fb, CHUNK_BYTES);
                     if (OP == LIN_FORWARD) tma_load_2d(code_base + c * CHUNK_BYTES, &qmap, fb, (int)(part * 32u), (int)i0);
                     else tma_load_2d(code_base + c * CHUNK_BYTES, &qmap, fb, (int)(Fmt<FMT>::four ? i0 / 2u : i0), (int)(part * 64u));
@@ -589,8 +656,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
             ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t i = t % pl.tiles_i * 128u + il, j0 = t / pl.tiles_i * bt;
-            const uint32_t cols = min(bt, a.nj - j0);
+            const uint32_t i = tile_i0(t) + il, j0 = t / pl.tiles_i * tile_j;
+            const uint32_t cols = min(tile_j, a.nj - j0);
             for (uint32_t c0 = 0; c0 < cols; c0 += 32u) {
                 uint32_t v[32];
                 tmem_ld32(tmem + b * ACC_COLS + ((q * 32u) << 16) + c0, v);
@@ -606,11 +673,15 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_first(smem_addr(&acc_empty[b]));
+                else mbar_arrive(smem_addr(&acc_empty[b]));
+            }
         }
     }
     __syncwarp();
-    if (pl.split > 1) {
+    if (PAIR) cluster_sync();                        // neither CTA leaves while the other's MMAs or arrivals may use it
+    if (!PAIR && pl.split > 1) {
         cluster_sync();
         // every CTA of the cluster adds up the parts of its share of the columns
         const uint32_t i = first % pl.tiles_i * 128u, j0 = first / pl.tiles_i * bt;
@@ -631,7 +702,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2u * ACC_COLS) : "memory");
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2u * ACC_COLS) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2u * ACC_COLS) : "memory");
     }
 }
 
@@ -676,7 +750,7 @@ uint32_t plan_stage_bytes(const MmaPlan& p) { return p.subs * (A_BYTES + p.bt * 
 
 // The tile width that takes the fewest rounds of tiles over the SMs, weighed by a round's
 // length (a stage costs bt, and no less than the 128 that widening its codes takes); then a
-// split of the contraction while tiles leave SMs idle and every part keeps four stages.
+// split of the contraction while tiles leave SMs idle and every CTA keeps a block of it.
 MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
 {
     MmaPlan p;
@@ -690,23 +764,33 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
         const uint64_t cost = ((tiles + sms - 1) / sms) * std::max(bt, 128u);
         if (cost < best) { best = cost; p.bt = bt; }
     }
-    p.tiles = p.tiles_i * ceil_div(a.nj, p.bt);
-    p.subs = p.bt > 128u ? 1u : 2u;
-    p.kt = ceil_div(a.nc, 64u * p.subs);
+    // pairs of CTAs where their larger tiles fill the SMs as well
+    const uint64_t pair_tiles = (uint64_t)ceil_div(a.ni, 256u) * ceil_div(a.nj, 256u);
+    const uint64_t pair_cost = ((pair_tiles + sms / 2 - 1) / (sms / 2)) * 256u;
+    p.pair = pair_tiles >= sms / 2 && pair_cost * 4 <= best * 5 ? 1u : 0u;
+    if (p.pair) {
+        p.bt = 128;
+        p.tiles_i = ceil_div(a.ni, 256u);
+        p.tiles = (uint32_t)pair_tiles;
+    } else {
+        p.tiles = p.tiles_i * ceil_div(a.nj, p.bt);
+    }
+    p.subs = p.bt > 128u || p.pair ? 1u : 2u;
+    p.blocks = ceil_div(a.nc, 256u);
     p.split = 1;
-    while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.kt * p.subs >= p.split * 2 * 4) p.split *= 2;
+    while (!p.pair && p.split < 8 && p.tiles * p.split * 2 <= sms && p.blocks >= p.split * 2) p.split *= 2;
     // two chunks of codes at least, up to four stages, then more chunks: with narrow tiles the
     // codes are most of what is read, and their ring keeps the memory busy
     const uint32_t room = SMEM_ROOM, stage = plan_stage_bytes(p);
-    p.stages = std::min(4u, (room - 2u * CHUNK_BYTES) / stage);          // times subs >= 4 parts (see there)
-    p.chunks = std::min<uint32_t>(MAX_CHUNKS, (room - p.stages * stage) / CHUNK_BYTES);
+    p.stages = std::min(p.pair ? 6u : 4u, (room - 2u * CHUNK_BYTES) / stage);          // times subs >= 4 parts (see there)
+    p.chunks = std::min<uint32_t>(MAX_CHUNKS, (room - p.stages * stage) / CHUNK_BYTES) & ~1u;
     return p;
 }
 
-template <int OP, int FMT, bool NV>
-cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
+template <int OP, int FMT, bool NV, bool PAIR>
+cudaError_t run_plan(const LinearArgs& a, const MmaPlan& pl, uint32_t sms, cudaStream_t st)
 {
-    constexpr auto kern = k_linear_mma<OP, FMT, NV>;
+    constexpr auto kern = k_linear_mma<OP, FMT, NV, PAIR>;
     static std::atomic<uint64_t> attr_set{0};        // a bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -717,15 +801,13 @@ cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set.fetch_or(bit, std::memory_order_acq_rel);
     }
-    const uint32_t sms = (uint32_t)device_sm_count();
-    const MmaPlan pl = make_mma_plan(OP, a, sms);
     CUtensorMap xm, qm;
     e = x_map(a, OP == LIN_GRAD_WEIGHT ? 64u : pl.bt, &xm);
     if (e != cudaSuccess) return e;
     e = codes_map(OP, Fmt<FMT>::four, a, &qm);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(pl.split > 1 ? pl.tiles * pl.split : std::min(pl.tiles, sms));
+    cfg.gridDim = dim3(PAIR ? 2u * std::min(pl.tiles, sms / 2u) : pl.split > 1 ? pl.tiles * pl.split : std::min(pl.tiles, sms));
     cfg.blockDim = dim3(MMA_THREADS);
     cfg.dynamicSmemBytes = pl.stages * plan_stage_bytes(pl) + pl.chunks * CHUNK_BYTES + 1024u;
     cfg.stream = st;
@@ -733,12 +815,20 @@ cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = pl.split;
+    at[1].val.clusterDim.x = PAIR ? 2u : pl.split;
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = pl.split > 1 ? 2 : 1;
+    cfg.numAttrs = PAIR || pl.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, xm, qm, a, pl);
+}
+
+template <int OP, int FMT, bool NV>
+cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
+{
+    const uint32_t sms = (uint32_t)device_sm_count();
+    const MmaPlan pl = make_mma_plan(OP, a, sms);
+    return pl.pair ? run_plan<OP, FMT, NV, true>(a, pl, sms, st) : run_plan<OP, FMT, NV, false>(a, pl, sms, st);
 }
 
 template <bool NV, int R>

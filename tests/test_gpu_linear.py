@@ -101,6 +101,38 @@ def test_grad_weight(s, shape):
         _close(bq.linear_grad_weight(dy.cuda(), q, dt), _f64(dy).T, xv, dt, m)
 
 
+# products large enough for tiles on pairs of SMs, one to three tiles each; ragged in every
+# direction (output rows, output columns, contraction length)
+@pytest.mark.parametrize("s", W_SCHEMES, ids=lambda s: s.gran)
+@pytest.mark.parametrize("shape", [(2560, 2048, 64), (1100, 4700, 96), (2100, 5001, 672)], ids=lambda t: "x".join(map(str, t)))
+def test_linear_many_tiles(s, shape):
+    m, n, k = shape
+    q, w = _weight(n, k, s, 950 + n)
+    x = _acts(m, k, 951 + m)
+    for dt in (torch.bfloat16, torch.float32):
+        _close(bq.linear(x.cuda(), q, dt), _f64(x), w.T, dt, k)
+
+
+@pytest.mark.parametrize("s", W_SCHEMES, ids=lambda s: s.gran)
+@pytest.mark.parametrize("shape", [(2560, 64, 2048), (1100, 201, 4640), (2100, 700, 4992)], ids=lambda t: "x".join(map(str, t)))
+def test_grad_input_many_tiles(s, shape):
+    m, n, k = shape
+    q, w = _weight(n, k, s, 952 + n)
+    dy = _acts(m, n, 953 + m)
+    for dt in (torch.bfloat16, torch.float32):
+        _close(bq.linear_grad_input(dy.cuda(), q, dt), _f64(dy), w, dt, n)
+
+
+@pytest.mark.parametrize("s", X_SCHEMES, ids=lambda s: s.fmt)
+@pytest.mark.parametrize("shape", [(64, 2560, 2048), (201, 1101, 4640), (700, 2100, 4992)], ids=lambda t: "x".join(map(str, t)))
+def test_grad_weight_many_tiles(s, shape):
+    m, n, k = shape
+    q, xv = _quantized(_acts(m, k, 954 + m), s)
+    dy = _acts(m, n, 955 + n)
+    for dt in (torch.bfloat16, torch.float32):
+        _close(bq.linear_grad_weight(dy.cuda(), q, dt), _f64(dy).T, xv, dt, m)
+
+
 # every row and block of the scales' tiled layout: more than 128 rows, several tiles of blocks
 @pytest.mark.parametrize("m", [1, 11, 40, 300])
 @pytest.mark.parametrize("s", [Scheme("e2m1", "mx", layout="gemm"), Scheme("e2m1", "nv", layout="gemm")],
