@@ -286,7 +286,7 @@ struct MmaPlan {
     uint32_t subs;          // 64-step parts of a stage: 1 or 2
     uint32_t stages;        // of the ring
     uint32_t chunks;        // of the code ring
-    uint32_t tiles_i, tiles;
+    uint32_t tiles_i, tiles_j, tiles;
     uint32_t blocks;        // of the contraction: 256 steps, four parts, each
     uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
     uint32_t pair;          // 1: tiles of 256 x 256 on pairs of CTAs (bt 128 each)
@@ -328,26 +328,15 @@ __device__ __forceinline__ void tc_commit_all(uint32_t bar)
         tc_commit(bar);
 }
 
-// Arrival on the first CTA's barrier (bar: its address in this CTA), and a wait that sees what
-// came before such arrivals.
+// Arrival on the first CTA's barrier (bar: its address in this CTA). Without a cluster-scope
+// release, which takes about 900 cycles (a pair's stages then took 1340 instead of 700): what
+// it hands over lies in this CTA's own shared memory and was made visible here before, by the
+// copies' completion or by the writers' proxy fence and arrivals, and is read by this SM's
+// tensor core.
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
 {
     asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %0, 0;\n"
-                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [p];\n}" :: "r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity)
-{
-    const uint64_t t0 = global_ns();
-    for (;;) {
-        for (int i = 0; i < 64; ++i) {
-            uint32_t ok;
-            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-                         " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
-            if (ok) return true;
-        }
-        if (global_ns() - t0 > WAIT_LIMIT_NS) return false;
-    }
+                 "mbarrier.arrive.shared::cluster.b64 _, [p];\n}" :: "r"(bar) : "memory");
 }
 
 // One lane of a converged warp.
@@ -377,6 +366,17 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %1, %2;\nld.shared::cluster.f32 %0, [p];\n}"
                  : "=f"(v) : "r"(addr), "r"(rank) : "memory");
     return v;
+}
+
+// Tile t: (tile of i, tile of j). Groups of 8 tiles of j, i by i, j fastest: the CTAs at work
+// at a time then read several tiles of X (with one, all of them asked the L2 for the same lines
+// at once, and the copies of X alone took as long as everything else: 525 of 487 us for 4096
+// tokens x 11008 x 4096) and few of Q.
+__device__ __forceinline__ uint2 tile_at(const MmaPlan& p, uint32_t t)
+{
+    const uint32_t per_group = 8u * p.tiles_i, grp = t / per_group, rem = t - grp * per_group;
+    const uint32_t j0 = grp * 8u, w = min(8u, p.tiles_j - j0);
+    return make_uint2(rem / w, j0 + rem % w);
 }
 
 template <int OP, int FMT, bool NV, bool PAIR>
@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     // parts past the contraction's end fill up its last block: they take part in every hand-over,
     // but nothing is copied, widened or multiplied for them
     auto live = [&](uint32_t part) { return (uint64_t)part * 64u < a.nc; };
-    // first i of a tile for this CTA
-    auto tile_i0 = [&](uint32_t t) { return t % pl.tiles_i * (PAIR ? 256u : 128u) + (PAIR ? rank * 128u : 0u); };
+    // first i of a tile for this CTA, and first j of the tile
+    auto tile_i0 = [&](uint32_t t) { return tile_at(pl, t).x * (PAIR ? 256u : 128u) + (PAIR ? rank * 128u : 0u); };
+    auto tile_j0 = [&](uint32_t t) { return tile_at(pl, t).y * tile_j; };
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < NS; ++s) {
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const bool leader = elect_one();
         uint32_t s = 0, round = 0;                   // slot of the ring, and how often it wrapped
         for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
-            const int j0 = (int)(t / pl.tiles_i * tile_j + (PAIR ? rank * bt : 0u));
+            const int j0 = (int)(tile_j0(t) + (PAIR ? rank * bt : 0u));
             for (uint32_t kk = 0; kk < tile_stages; ++kk) {
                 if (round > 0 && !mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u)) { abort_flag = 1; break; }
                 if (abort_flag) break;
@@ -494,7 +495,6 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint32_t idesc = mma_desc<OP>(PAIR ? 256u : 128u, tile_j);
         const uint64_t ad0 = OP == LIN_FORWARD ? operand_desc(base) : mn_desc(base);
         const uint64_t bd0 = OP == LIN_GRAD_WEIGHT ? mn_desc(base + A_BYTES) : operand_desc(base + A_BYTES);
-        auto wait = [](uint32_t bar, uint32_t parity) { return PAIR ? mbar_wait_pair(bar, parity) : mbar_wait_ring(bar, parity); };
         uint32_t s = 0, par = 0, i = 0;
         if (PAIR && rank != 0) {
             // the second CTA of a pair only says when its half of a stage is there
@@ -510,12 +510,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         } else {
             for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
                 const uint32_t b = i & 1u;
-                if (i >= 2 && !wait(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
+                if (i >= 2 && !mbar_wait_ring(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + b * ACC_COLS;
                 uint32_t acc = 0;
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
-                    if (!wait(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
+                    if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
                     if (abort_flag) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     for (uint32_t u = 0; u < subs; ++u) {
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
             ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t i = tile_i0(t) + il, j0 = t / pl.tiles_i * tile_j;
+            const uint32_t i = tile_i0(t) + il, j0 = tile_j0(t);
             const uint32_t cols = min(tile_j, a.nj - j0);
             for (uint32_t c0 = 0; c0 < cols; c0 += 32u) {
                 uint32_t v[32];
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     if (!PAIR && pl.split > 1) {
         cluster_sync();
         // every CTA of the cluster adds up the parts of its share of the columns
-        const uint32_t i = first % pl.tiles_i * 128u, j0 = first / pl.tiles_i * bt;
+        const uint32_t i = tile_i0(first), j0 = tile_j0(first);
         const uint32_t from = bt * rank / pl.split, to = min(bt * (rank + 1) / pl.split, a.nj - j0);
         const float sc = out_scale<NV>(a);
         for (uint32_t o = from * 128u + threadIdx.x; o < to * 128u; o += MMA_THREADS) {
@@ -771,10 +771,9 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     if (p.pair) {
         p.bt = 128;
         p.tiles_i = ceil_div(a.ni, 256u);
-        p.tiles = (uint32_t)pair_tiles;
-    } else {
-        p.tiles = p.tiles_i * ceil_div(a.nj, p.bt);
     }
+    p.tiles_j = ceil_div(a.nj, p.pair ? 256u : p.bt);
+    p.tiles = p.tiles_i * p.tiles_j;
     p.subs = p.bt > 128u || p.pair ? 1u : 2u;
     p.blocks = ceil_div(a.nc, 256u);
     p.split = 1;
