@@ -2,8 +2,8 @@
 // gradients): out[j, i] = sum_c X(j, c) Q(i, c), X bf16, Q block-scaled codes, the roles of
 // the stored matrices as LinearArgs says.
 //
-// Every code times its block scale is a bf16 value (widen.cuh), so the codes are widened to
-// bf16 on the way to the tensor cores and the products with X are exact; sums are fp32.
+// Every code times its block scale is a bf16 value (widen.cuh), so the codes are widened on the
+// way to the tensor cores and the products with X are exact; sums are fp32.
 //
 // Two kernels:
 //  - k_linear_mma, on the fifth-generation tensor cores: out's transpose in tiles of 128
@@ -774,7 +774,7 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     }
     p.tiles_j = ceil_div(a.nj, p.pair ? 256u : p.bt);
     p.tiles = p.tiles_i * p.tiles_j;
-    p.subs = p.bt > 128u || p.pair ? 1u : 2u;
+    p.subs = p.bt > 128u ? 1u : 2u;
     p.blocks = ceil_div(a.nc, 256u);
     p.split = 1;
     while (!p.pair && p.split < 8 && p.tiles * p.split * 2 <= sms && p.blocks >= p.split * 2) p.split *= 2;
@@ -786,20 +786,27 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     return p;
 }
 
+// Lets kern use up to bytes of dynamic shared memory on the current device (once per device).
+template <typename K>
+cudaError_t allow_smem(K kern, uint32_t bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0u;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
 template <int OP, int FMT, bool NV, bool PAIR>
 cudaError_t run_plan(const LinearArgs& a, const MmaPlan& pl, uint32_t sms, cudaStream_t st)
 {
     constexpr auto kern = k_linear_mma<OP, FMT, NV, PAIR>;
     static std::atomic<uint64_t> attr_set{0};        // a bit per device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = allow_smem(kern, SMEM_MAX - 1024u, attr_set);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(attr_set.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(SMEM_MAX - 1024u));
-        if (e != cudaSuccess) return e;
-        if (dev < 64) attr_set.fetch_or(bit, std::memory_order_acq_rel);
-    }
     CUtensorMap xm, qm;
     e = x_map(a, OP == LIN_GRAD_WEIGHT ? 64u : pl.bt, &xm);
     if (e != cudaSuccess) return e;
