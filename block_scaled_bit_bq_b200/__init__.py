@@ -531,6 +531,11 @@ def _c_scheme(scheme: Scheme) -> BqScheme:
     return c
 
 
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream of dev (torch.cuda.current_stream(dev).cuda_stream without the object)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _elsewhere(dev: torch.device, stream) -> bool:
     if dev.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
@@ -553,37 +558,33 @@ def _on(dev: torch.device, stream):
             yield
 
 
-def _check_operand(t: torch.Tensor, name: str, cols: int, dev: torch.device) -> None:
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+def _operand(t: torch.Tensor, name: str, rows: int | None, cols: int, dev: torch.device, step: int):
+    """(t or a copy of it, elements between its rows): bf16 [rows, cols] on dev with unit column
+    stride, rows a multiple of step elements apart and the first element 2 * step bytes
+    aligned. (A tensor of at most one row, or of none to a row, has no such distance: any
+    valid value.)"""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D bf16 CUDA tensor")
-    if t.shape[1] != cols:
-        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    r, c = t.shape
+    if c != cols or (rows is not None and r != rows):
+        raise ValueError(f"{name} is [{r}, {c}], expected [{'any' if rows is None else rows}, {cols}]")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the codes on {dev}")
-
-
-def _ld(t: torch.Tensor, step: int) -> int:
-    """Elements between t's rows (a tensor of at most one row, or of none to a row, has no
-    such distance: any valid value)."""
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] else -(-t.shape[1] // step) * step
-
-
-def _rows_apart(t: torch.Tensor, step: int) -> torch.Tensor:
-    """t, or a copy of it, with unit column stride, rows a multiple of step elements apart
-    and the first element 2 * step bytes aligned."""
-    rows, cols = t.shape
-    ld = _ld(t, step)
-    if (t.stride(1) == 1 or cols == 1) and ld >= cols and ld % step == 0 and t.data_ptr() % (2 * step) == 0:
-        return t
-    buf = torch.empty((rows, -(-cols // step) * step), dtype=t.dtype, device=t.device)[:, :cols]
+    ld, s1 = t.stride()
+    if r <= 1 or c == 0:
+        ld = -(-c // step) * step
+    if (s1 == 1 or c == 1) and ld >= c and ld % step == 0 and t.data_ptr() % (2 * step) == 0:
+        return t, ld
+    ld = -(-c // step) * step
+    buf = torch.empty((r, ld), dtype=t.dtype, device=dev)[:, :c]
     buf.copy_(t)
-    return buf
+    return buf, ld
 
 
 def _out(out: torch.Tensor | None, rows: int, cols: int, dtype, dev: torch.device) -> torch.Tensor:
-    if dtype not in _OUT_DT:
-        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
     if out is None:
+        if dtype not in _OUT_DT:
+            raise ValueError("dtype must be torch.bfloat16 or torch.float32")
         return torch.empty((rows, cols), dtype=dtype, device=dev)
     if out.shape != (rows, cols) or out.dtype not in _OUT_DT or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous bf16 or fp32 [{rows}, {cols}] tensor on {dev}")
@@ -598,13 +599,12 @@ def linear(x: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tenso
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear(x, w, dtype, out)
-    _check_operand(x, "x", w.cols, dev)
-    x = _rows_apart(x, 8)
-    m = x.shape[0]
-    y = _out(out, m, w.rows, dtype, dev)
-    _check(_lib().bq_linear(x.data_ptr(), 0, _ld(x, 8), w.codes.data_ptr(), w.scales.data_ptr(),
-                            _ptr(w.tensor_scale), m, w.rows, w.cols, ctypes.byref(_c_scheme(w.scheme)), y.data_ptr(),
-                            _OUT_DT[y.dtype], _stream(None)), "bq_linear")
+    x, ld = _operand(x, "x", None, w.cols, dev, 8)
+    m, n = x.shape[0], w.rows
+    y = _out(out, m, n, dtype, dev)
+    _check(_lib().bq_linear(x.data_ptr(), 0, ld, w.codes.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale), m, n,
+                            w.cols, ctypes.byref(_c_scheme(w.scheme)), y.data_ptr(), _OUT_DT[y.dtype],
+                            _raw_stream(dev)), "bq_linear")
     return y
 
 
@@ -615,13 +615,12 @@ def linear_grad_input(dy: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out:
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear_grad_input(dy, w, dtype, out)
-    _check_operand(dy, "dy", w.rows, dev)
-    dy = _rows_apart(dy, 8)
-    m = dy.shape[0]
-    dx = _out(out, m, w.cols, dtype, dev)
-    _check(_lib().bq_linear_grad_input(dy.data_ptr(), 0, _ld(dy, 8), w.codes.data_ptr(), w.scales.data_ptr(),
-                                       _ptr(w.tensor_scale), m, w.rows, w.cols, ctypes.byref(_c_scheme(w.scheme)),
-                                       dx.data_ptr(), _OUT_DT[dx.dtype], _stream(None)), "bq_linear_grad_input")
+    dy, ld = _operand(dy, "dy", None, w.rows, dev, 8)
+    m, k = dy.shape[0], w.cols
+    dx = _out(out, m, k, dtype, dev)
+    _check(_lib().bq_linear_grad_input(dy.data_ptr(), 0, ld, w.codes.data_ptr(), w.scales.data_ptr(),
+                                       _ptr(w.tensor_scale), m, w.rows, k, ctypes.byref(_c_scheme(w.scheme)),
+                                       dx.data_ptr(), _OUT_DT[dx.dtype], _raw_stream(dev)), "bq_linear_grad_input")
     return dx
 
 
@@ -633,16 +632,29 @@ def linear_grad_weight(dy: torch.Tensor, x: Quantized, dtype=torch.float32, out:
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear_grad_weight(dy, x, dtype, out)
-    if dy.dim() != 2 or dy.shape[0] != x.rows:
-        raise ValueError(f"dy must be [{x.rows}, n], as many rows as the kept input")
-    n = dy.shape[1]
-    _check_operand(dy, "dy", n, dev)
-    dy = _rows_apart(dy, 8)
-    dw = _out(out, n, x.cols, dtype, dev)
-    _check(_lib().bq_linear_grad_weight(dy.data_ptr(), 0, _ld(dy, 8), x.codes.data_ptr(), x.scales.data_ptr(), x.rows,
-                                        n, x.cols, ctypes.byref(_c_scheme(x.scheme)), dw.data_ptr(), _OUT_DT[dw.dtype],
-                                        _stream(None)), "bq_linear_grad_weight")
+    dy, ld = _operand(dy, "dy", x.rows, dy.shape[-1], dev, 8)
+    n, k = dy.shape[1], x.cols
+    dw = _out(out, n, k, dtype, dev)
+    _check(_lib().bq_linear_grad_weight(dy.data_ptr(), 0, ld, x.codes.data_ptr(), x.scales.data_ptr(), x.rows, n, k,
+                                        ctypes.byref(_c_scheme(x.scheme)), dw.data_ptr(), _OUT_DT[dw.dtype],
+                                        _raw_stream(dev)), "bq_linear_grad_weight")
     return dw
+
+
+def _resolved(scheme: Scheme) -> Scheme:
+    """scheme.resolved(), kept on the scheme like its C form."""
+    r = scheme.__dict__.get("_r")
+    if r is None:
+        r = scheme.resolved()
+        object.__setattr__(scheme, "_r", r)
+    return r
+
+
+def _glu_copy(s: Scheme, rows: int, cols: int, dev: torch.device) -> Quantized:
+    """Buffers of one 8-bit MX copy (alloc_outputs of the schemes that bq_glu takes; the others
+    it refuses before they are written)."""
+    return Quantized(s, rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                     torch.empty(max(rows * cols // 32, 1), dtype=torch.uint8, device=dev), None, None, None)
 
 
 @dataclass
@@ -665,30 +677,32 @@ def glu(gate: torch.Tensor, up: torch.Tensor, scheme: Scheme | None = None, act:
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return glu(gate, up, scheme, act, out, ckpt)
-    _check_operand(gate, "gate", cols, dev)
-    _check_operand(up, "up", cols, dev)
-    gate, up = _rows_apart(gate, 16), _rows_apart(up, 16)
+    gate, ldg = _operand(gate, "gate", rows, cols, dev, 16)
+    up, ldu = _operand(up, "up", rows, cols, dev, 16)
     h = _out(out, rows, cols, torch.bfloat16, dev)
-    if h.dtype != torch.bfloat16:
+    if h.dtype is not torch.bfloat16:
         raise ValueError("out must be bf16")
     if scheme is None:
         if ckpt is not None:
             raise ValueError("a checkpoint needs a scheme")
-        _check(_lib().bq_glu(gate.data_ptr(), _ld(gate, 16), up.data_ptr(), _ld(up, 16), 0, rows, cols, ACTS[act],
-                             h.data_ptr(), None, None, None, None, None, _stream(None)), "bq_glu")
+        _check(_lib().bq_glu(gate.data_ptr(), ldg, up.data_ptr(), ldu, 0, rows, cols, ACTS[act], h.data_ptr(), None, None,
+                             None, None, None, _raw_stream(dev)), "bq_glu")
         return h, None
+    a = ACTS[act]
     if ckpt is None:
-        ckpt = GluCheckpoint(alloc_outputs(scheme, rows, cols, dev, False),
-                             alloc_outputs(scheme, rows, cols, dev, False), act)
-    s, g, u = scheme.resolved(), ckpt.gate, ckpt.up
-    if g.scheme != s or u.scheme != s or (g.rows, g.cols) != (rows, cols) or (u.rows, u.cols) != (rows, cols):
-        raise ValueError("the checkpoint's buffers are of another scheme or shape")
-    if g.codes.device != dev or u.codes.device != dev:
-        raise ValueError(f"the checkpoint's buffers are not on {dev}")
-    ckpt.act = act
-    _check(_lib().bq_glu(gate.data_ptr(), _ld(gate, 16), up.data_ptr(), _ld(up, 16), 0, rows, cols, ACTS[act],
-                         h.data_ptr(), ctypes.byref(_c_scheme(s)), g.codes.data_ptr(), g.scales.data_ptr(),
-                         u.codes.data_ptr(), u.scales.data_ptr(), _stream(None)), "bq_glu")
+        s = _resolved(scheme)
+        g, u = _glu_copy(s, rows, cols, dev), _glu_copy(s, rows, cols, dev)
+        ckpt = GluCheckpoint(g, u, act)
+    else:
+        s, g, u = scheme.resolved(), ckpt.gate, ckpt.up
+        if g.scheme != s or u.scheme != s or (g.rows, g.cols) != (rows, cols) or (u.rows, u.cols) != (rows, cols):
+            raise ValueError("the checkpoint's buffers are of another scheme or shape")
+        if g.codes.device != dev or u.codes.device != dev:
+            raise ValueError(f"the checkpoint's buffers are not on {dev}")
+        ckpt.act = act
+    _check(_lib().bq_glu(gate.data_ptr(), ldg, up.data_ptr(), ldu, 0, rows, cols, a, h.data_ptr(),
+                         ctypes.byref(_c_scheme(s)), g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(),
+                         u.scales.data_ptr(), _raw_stream(dev)), "bq_glu")
     return h, ckpt
 
 
@@ -701,20 +715,19 @@ def glu_backward(dh: torch.Tensor, ckpt: GluCheckpoint, out=None, stream=None):
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return glu_backward(dh, ckpt, out)
-    if dh.dim() != 2 or dh.shape[0] != rows or (u.rows, u.cols, u.scheme) != (rows, cols, g.scheme):
-        raise ValueError("dh and the two copies must be of one shape")
-    _check_operand(dh, "dh", cols, dev)
-    dh = _rows_apart(dh, 16)
+    if (u.rows, u.cols) != (rows, cols) or u.scheme != g.scheme or u.codes.device != dev:
+        raise ValueError("the two copies must be of one shape and scheme, on one device")
+    dh, ldh = _operand(dh, "dh", rows, cols, dev, 16)
     if out is None:
-        out = (torch.empty((rows, cols), dtype=torch.bfloat16, device=dev),
-               torch.empty((rows, cols), dtype=torch.bfloat16, device=dev))
-    dg, du = out
-    for t in (dg, du):
-        _check_operand(t, "out", cols, dev)
-        if t.shape[0] != rows or (t.stride(1) != 1 and cols > 1):
-            raise ValueError(f"out must be [{rows}, {cols}] tensors with unit column stride")
-    _check(_lib().bq_glu_backward(dh.data_ptr(), _ld(dh, 16), 0, g.codes.data_ptr(), g.scales.data_ptr(),
-                                  u.codes.data_ptr(), u.scales.data_ptr(), ctypes.byref(_c_scheme(g.scheme)), rows,
-                                  cols, ACTS[ckpt.act], dg.data_ptr(), _ld(dg, 16), du.data_ptr(), _ld(du, 16),
-                                  _stream(None)), "bq_glu_backward")
+        dg = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        du = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        ldg = ldu = cols
+    else:
+        dg, du = out
+        (tg, ldg), (tu, ldu) = _operand(dg, "out", rows, cols, dev, 16), _operand(du, "out", rows, cols, dev, 16)
+        if tg is not dg or tu is not du:
+            raise ValueError("out must have unit column stride, rows a multiple of 16 elements apart and be 32-byte aligned")
+    _check(_lib().bq_glu_backward(dh.data_ptr(), ldh, 0, g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(),
+                                  u.scales.data_ptr(), ctypes.byref(_c_scheme(g.scheme)), rows, cols, ACTS[ckpt.act],
+                                  dg.data_ptr(), ldg, du.data_ptr(), ldu, _raw_stream(dev)), "bq_glu_backward")
     return dg, du
