@@ -359,12 +359,31 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A float of another CTA's shared memory (addr: the same variable's address in this CTA).
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
+// Four floats of another CTA's shared memory (addr: the same variable's address in this CTA).
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank)
 {
-    float v;
-    asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %1, %2;\nld.shared::cluster.f32 %0, [p];\n}"
-                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    float4 v;
+    asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %4, %5;\nld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [p];\n}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank));
+    return v;
+}
+
+// The sum over S ranks, in order, of four floats at the same place in each; all loads are under
+// way before the first is used (one after the other, they took most of a small product's time).
+template <int S>
+__device__ __forceinline__ float4 sum_cluster(uint32_t addr)
+{
+    float4 p[S];
+#pragma unroll
+    for (int r = 0; r < S; ++r) p[r] = ld_cluster(addr, (uint32_t)r);
+    float4 v = p[0];
+#pragma unroll
+    for (int r = 1; r < S; ++r) {
+        v.x = __fadd_rn(v.x, p[r].x);
+        v.y = __fadd_rn(v.y, p[r].y);
+        v.z = __fadd_rn(v.z, p[r].z);
+        v.w = __fadd_rn(v.w, p[r].w);
+    }
     return v;
 }
 
@@ -687,12 +706,15 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint32_t i = tile_i0(first), j0 = tile_j0(first);
         const uint32_t from = bt * rank / pl.split, to = min(bt * (rank + 1) / pl.split, a.nj - j0);
         const float sc = out_scale<NV>(a);
-        for (uint32_t o = from * 128u + threadIdx.x; o < to * 128u; o += MMA_THREADS) {
-            const uint32_t ii = i + (o & 127u);
+        for (uint32_t o = from * 128u + threadIdx.x * 4u; o < to * 128u; o += MMA_THREADS * 4u) {
+            const uint32_t ii = i + (o & 127u), at = base + o * 4u;
             if (ii >= a.ni) continue;
-            float v = 0.0f;
-            for (uint32_t rk = 0; rk < pl.split; ++rk) v = __fadd_rn(v, ld_cluster(base + o * 4u, rk));
-            store_out(a, (size_t)(j0 + (o >> 7)) * a.ni + ii, NV ? __fmul_rn(v, sc) : v);
+            const float4 v = pl.split == 2 ? sum_cluster<2>(at) : pl.split == 4 ? sum_cluster<4>(at) : sum_cluster<8>(at);
+            const float e[4] = {v.x, v.y, v.z, v.w};
+            const size_t oo = (size_t)(j0 + (o >> 7)) * a.ni + ii;
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c)
+                if (ii + c < a.ni) store_out(a, oo + c, NV ? __fmul_rn(e[c], sc) : e[c]);
         }
         cluster_sync();                              // no CTA leaves while its parts are being read
     }
