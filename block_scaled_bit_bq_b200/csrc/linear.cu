@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         code_empty[MAX_CHUNKS], acc_full[2], acc_empty[2], done_bar;
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    // (from lane 0, so that the compiler sees the warps' roles as uniform branches)
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     const uint32_t base = (smem_addr(linear_smem) + 1023u) & ~1023u;
     // bt: the j that this CTA copies; a pair's tile has twice as many
     const uint32_t bt = pl.bt, subs = pl.subs, NS = pl.stages;
