@@ -69,10 +69,8 @@ __device__ __forceinline__ uint32_t load_scale(const LinearArgs& a, uint32_t row
 // load where a row's scales start on a multiple of its size (wide). The loaded words are taken
 // apart only where they are used (pair_scale): doing so here would wait for them.
 template <bool NV>
-__device__ __forceinline__ void load_scale_pair(const LinearArgs& a, uint32_t row, uint32_t grp, bool wide, bool second,
-                                                uint32_t (&s)[2])
+__device__ __forceinline__ void load_scale_pair(const uint8_t* p, bool wide, bool second, uint32_t (&s)[2])
 {
-    const uint8_t* p = a.scales + scale_offset(a, row, NV ? 2 * grp : grp);
     if (wide) {
         s[0] = NV ? ldg_u32(p) : ldg_u16(p);
     } else {
@@ -207,8 +205,9 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 uint32_t p0[16], p1[16];
-                W::pairs(w[p][2 * r], s[p][2 * r], p0);
-                W::pairs(w[p][2 * r + 1], s[p][2 * r + 1], p1);
+                const bool one = __all_sync(0xFFFFFFFFu, W::fits(s[p][2 * r]) && W::fits(s[p][2 * r + 1]));
+                W::pairs(w[p][2 * r], s[p][2 * r], one, p0);
+                W::pairs(w[p][2 * r + 1], s[p][2 * r + 1], one, p1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -536,7 +535,6 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 uint32_t acc = 0;
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
                     if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
-                    if (abort_flag) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     for (uint32_t u = 0; u < subs; ++u) {
                         const uint64_t so = (s * stage_bytes + u * sub_bytes) >> 4, ad = ad0 + so, bd = bd0 + so;
@@ -569,53 +567,68 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         // parts or more, the code ring two chunks or more (of 8-bit codes, an even number) ----
         const uint32_t g = (warp - 2u) / GROUP_WARPS, tid = (threadIdx.x - 64u) % GROUP_THREADS;
         const uint32_t r = OP == LIN_FORWARD ? tid : tid & 63u, h = OP == LIN_FORWARD ? 0u : tid >> 6;
-        // where its codes lie in a chunk: row cr of 128 (or 64) bytes, 16-byte units from cu on
+        // where its codes lie in a chunk: row cr of 128 (or 64) bytes, 16-byte units from cu on (a
+        // multiple of their number, so that unit e is at the first one's address xor 16 e)
         const uint32_t cr = OP == LIN_FORWARD ? r : (g % CP) * 64u + r;
         const uint32_t cu = OP == LIN_FORWARD ? 2u * g : (Fmt<FMT>::four ? 2u * h : 4u * h);
-        const uint32_t c_row = cr * (OP == LIN_GRAD_INPUT ? 64u : 128u), c_xor = OP == LIN_GRAD_INPUT ? (cr >> 1) & 3u : cr & 7u;
-        const uint32_t dst_off = (g % subs) * sub_bytes + h * 8192u + r * 128u;
+        const uint32_t src_off = cr * (OP == LIN_GRAD_INPUT ? 64u : 128u) +
+                                 ((cu ^ (OP == LIN_GRAD_INPUT ? (cr >> 1) & 3u : cr & 7u)) << 4);
+        // where its values go: a row of 128 bytes, unit e at e ^ (r % 8)
+        const uint32_t dst_off = (g % subs) * sub_bytes + h * 8192u + r * 128u + ((r & 7u) << 4);
         const uint32_t groups = a.k / 32u;
         const bool wide = a.gemm_layout || (NV ? a.nb % 4u == 0 : a.nb % 2u == 0);
-        constexpr int P = 2;
-        uint32_t ld_tile = first, ld_pk = g, ld_i0 = tile_i0(first);   // the next part whose scales
-        uint32_t sc[P][2];                                           // are to be loaded
+        // the scales, two of this group's parts ahead: of row ld_row, 32-code groups ld_grp and + 1.
+        // From part to part the pointer goes by a fixed step: 8 groups along a row, or 256 rows
+        constexpr uint32_t GB = NV ? 2u : 1u;                 // bytes of a group
+        const size_t ld_step = OP == LIN_FORWARD ? (a.gemm_layout ? 2u * GB * 512u : 8u * GB)
+                                                 : (a.gemm_layout ? (size_t)2u * (a.nb / 4u) * 512u : (size_t)256u * a.nb);
+        uint32_t ld_tile = first, ld_pk = g, ld_row = 0, ld_grp = 0;
+        const uint8_t* ld_p = nullptr;
+        auto start_tile = [&]() {
+            if (ld_tile >= pl.tiles) return;
+            const uint32_t i0 = tile_i0(ld_tile), kk = p0 + g;
+            ld_row = OP == LIN_FORWARD ? i0 + r : kk * 64u + r;
+            ld_grp = OP == LIN_FORWARD ? kk * 2u : i0 / 32u + 2u * h;
+            ld_p = a.scales + scale_offset(a, ld_row, GB * ld_grp);
+        };
+        start_tile();
+        uint32_t sc[2][2];
         auto fetch = [&](uint32_t (&cs)[2]) {
             cs[0] = cs[1] = 0u;
+            if (ld_tile < pl.tiles && ld_row < a.q_rows && ld_grp < groups) load_scale_pair<NV>(ld_p, wide, ld_grp + 1u < groups, cs);
+            ld_p += ld_step;
+            if (OP == LIN_FORWARD) ld_grp += 8u;
+            else ld_row += 256u;
+            ld_pk += WIDEN_GROUPS;
             if (ld_pk >= kts) {
                 ld_pk = g;
                 ld_tile += step;
-                ld_i0 = tile_i0(ld_tile);
+                start_tile();
             }
-            if (ld_tile < pl.tiles && ld_pk < kts) {
-                const uint32_t kk = p0 + ld_pk;
-                const uint32_t row = OP == LIN_FORWARD ? ld_i0 + r : kk * 64u + r;
-                const uint32_t grp = OP == LIN_FORWARD ? kk * 2u : ld_i0 / 32u + 2u * h;
-                if (row < a.q_rows && grp < groups) load_scale_pair<NV>(a, row, grp, wide, grp + 1u < groups, cs);
-            }
-            ld_pk += WIDEN_GROUPS;
         };
-#pragma unroll
-        for (int p = 0; p < P; ++p) fetch(sc[p]);
+        fetch(sc[0]);
+        fetch(sc[1]);
         uint32_t s = g / subs, round = 0, c = g / CP, c_par = 0;      // slots of the two rings
         bool ok = true;
         for (uint32_t t = first; t < pl.tiles && ok; t += step) {
             for (uint32_t pk = g; pk < kts && ok; pk += WIDEN_GROUPS) {
                 ok = mbar_wait_ring(smem_addr(&code_full[c]), c_par);
-                const uint32_t src = code_base + c * CHUNK_BYTES + c_row;
+                const uint32_t src = code_base + c * CHUNK_BYTES + src_off;
                 uint32_t o[2][16], w[2][W::WORDS];
 #pragma unroll
                 for (uint32_t x = 0; x < 2; ++x)
 #pragma unroll
                     for (uint32_t e = 0; e < W::WORDS / 4; ++e)
-                        lds_v4(src + (((cu + x * (W::WORDS / 4) + e) ^ c_xor) << 4), w[x][4 * e], w[x][4 * e + 1],
-                               w[x][4 * e + 2], w[x][4 * e + 3]);
+                        lds_v4(src ^ ((x * (W::WORDS / 4) + e) << 4), w[x][4 * e], w[x][4 * e + 1], w[x][4 * e + 2],
+                               w[x][4 * e + 3]);
                 const uint32_t s0 = pair_scale<NV>(sc[0], wide, 0), s1 = pair_scale<NV>(sc[0], wide, 1);
                 sc[0][0] = sc[1][0];
                 sc[0][1] = sc[1][1];
+                const bool one = __all_sync(0xFFFFFFFFu, W::fits(s0) && W::fits(s1));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t v[W::WORDS * W::RAW];
-                    W::pairs(w[x], x ? s1 : s0, v);
+                    W::pairs(w[x], x ? s1 : s0, one, v);
                     W::in_order(v, o[x]);
                 }
                 __syncwarp();
@@ -628,8 +641,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                     const uint32_t dst = base + s * stage_bytes + dst_off;
 #pragma unroll
                     for (uint32_t e = 0; e < 8; ++e)
-                        sts_v4(dst + ((e ^ (r & 7u)) << 4), o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1],
-                               o[e >> 2][4 * (e & 3) + 2], o[e >> 2][4 * (e & 3) + 3]);
+                        sts_v4(dst ^ (e << 4), o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1], o[e >> 2][4 * (e & 3) + 2],
+                               o[e >> 2][4 * (e & 3) + 3]);
                     fence_proxy_async();
                 }
                 __syncwarp();

@@ -67,23 +67,26 @@ struct Widen {
         }
     }
 
+    // Whether a block's scale and the missing factor are one multiplier.
+    static __device__ __forceinline__ bool fits(uint32_t scale) { return OFF == 0 || NV || scale <= LIMIT; }
+
     // The raw pairs of all words times their blocks' scales. scale: the MX byte, or the two NV
-    // bytes (first block's low).
-    static __device__ __forceinline__ void pairs(const uint32_t (&w)[WORDS], uint32_t scale, uint32_t (&p)[WORDS * RAW])
+    // bytes (first block's low). one: fits(scale), or false for any scale (a warp decides for
+    // all its lanes).
+    static __device__ __forceinline__ void pairs(const uint32_t (&w)[WORDS], uint32_t scale, bool one,
+                                                 uint32_t (&p)[WORDS * RAW])
     {
-        uint32_t m[2];
-        bool fits = true;
-        if constexpr (NV) {
-            // E4M3 bits as bf16: s 2^-120; times 2^119 twice: s 2^118, which times 2^-126 leaves 2^-8
-            const uint32_t b = ((scale & 0xFFu) << 4) | ((scale & 0xFF00u) << 12);
-            const uint32_t s2 = bf2_mul(bf2_mul(b, 0x7B007B00u), 0x7B007B00u);
-            m[0] = __byte_perm(s2, s2, 0x1010);
-            m[1] = __byte_perm(s2, s2, 0x3232);
-        } else {
-            fits = scale <= LIMIT;
-            m[0] = m[1] = OFF ? (scale + OFF) * 0x00800080u : bf2_exp(scale);
-        }
-        if (OFF == 0 || NV || fits) {
+        if (NV || one) {
+            uint32_t m[2];
+            if constexpr (NV) {
+                // E4M3 bits as bf16: s 2^-120; times 2^119 twice: s 2^118, which times 2^-126 leaves 2^-8
+                const uint32_t b = ((scale & 0xFFu) << 4) | ((scale & 0xFF00u) << 12);
+                const uint32_t s2 = bf2_mul(bf2_mul(b, 0x7B007B00u), 0x7B007B00u);
+                m[0] = __byte_perm(s2, s2, 0x1010);
+                m[1] = __byte_perm(s2, s2, 0x3232);
+            } else {
+                m[0] = m[1] = OFF ? (scale + OFF) * 0x00800080u : bf2_exp(scale);
+            }
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
                 uint32_t r[RAW];
@@ -92,7 +95,7 @@ struct Widen {
                 for (int j = 0; j < RAW; ++j) p[i * RAW + j] = bf2_mul(r[j], m[i >= WORDS / 2]);
             }
         } else {
-            // a scale above 2^(127 - OFF): the power and the scale one after the other
+            // the missing power and the scale one after the other
             const uint32_t off = (127u + OFF) * 0x00800080u, e = bf2_exp(scale);
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
