@@ -140,8 +140,8 @@ __device__ __forceinline__ uint4 ldg_x(const void* p)
     return v;
 }
 
-template <bool NV, int R, int MT, int D>
-__global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArgs a)
+template <bool NV, int R, int MT>
+__global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear_rows(const LinearArgs a)
 {
     using W = Widen<BQ_FP4_E2M1, NV>;
     constexpr uint32_t TS = 16 * R + 4;              // floats from token to token: conflict-free
@@ -158,12 +158,15 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[r][t][e] = 0.0f;
 
-    uint32_t rows[2 * R];
-    bool live[2 * R];
+    // Rows past the last and columns past the end read the last ones instead: those rows are not
+    // stored, and those columns meet zeros of x.
+    constexpr uint32_t GB = NV ? 2u : 1u;                        // scale bytes of 32 codes
+    const uint8_t *code[2 * R], *scale[2 * R];
 #pragma unroll
     for (int h = 0; h < 2 * R; ++h) {
-        rows[h] = row0 + 8u * h + g;
-        live[h] = rows[h] < a.ni;
+        const uint32_t row = min(row0 + 8u * h + g, a.ni - 1u);
+        code[h] = a.codes + (size_t)row * (a.k / 2);
+        scale[h] = a.scales + scale_offset(a, row, 0u);
     }
     const uint16_t* xr[MT];
     bool tok[MT];
@@ -174,54 +177,47 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) k_linear_rows(const LinearArg
         xr[t] = reinterpret_cast<const uint16_t*>(a.x) + (tok[t] ? j : 0u) * a.ldx;
     }
 
-    // the loads of D pieces ahead of the one being multiplied
-    uint32_t w[D][2 * R][4], s[D][2 * R];
-    uint4 x[D][MT][4];
-    auto fetch = [&](uint32_t grp, uint32_t (&cw)[2 * R][4], uint32_t (&cs)[2 * R], uint4 (&cx)[MT][4]) {
-        const bool in = grp < groups;
+    // a piece's loads; other warps (three CTAs an SM, two with 32 rows or 16 tokens) work meanwhile
+    uint32_t w[2 * R][4], s[2 * R];
+    uint4 x[MT][4];
+    auto fetch = [&](uint32_t next) {
+        const bool in = next < groups;
+        const uint32_t grp = min(next, groups - 1u);
+        // block grp * GB of a row: in the tiled layout four to a tile of 512 bytes
+        const uint32_t so = a.gemm_layout ? ((grp * GB) >> 2) * 512u + ((grp * GB) & 3u) : grp * GB;
 #pragma unroll
         for (int h = 0; h < 2 * R; ++h) {
-            cs[h] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cw[h][i] = 0u;
-            if (in && live[h]) {
-                ld_nc_v4(a.codes + (size_t)rows[h] * (a.k / 2) + grp * 16u, cw[h]);
-                cs[h] = load_scale<NV>(a, rows[h], grp);
-            }
+            ld_nc_v4(code[h] + (size_t)grp * 16u, w[h]);
+            s[h] = NV ? ldg_u16(scale[h] + so) : ldg_u8(scale[h] + so);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                cx[t][i] = in && tok[t] ? ldg_x(xr[t] + grp * 32u + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                x[t][i] = in && tok[t] ? ldg_x(xr[t] + grp * 32u + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
     };
-    constexpr uint32_t STEP = 4u * ROWS_WARPS;
     const uint32_t g0 = 4u * warp + q;
+    if (4u * warp < groups) fetch(g0);
+    for (uint32_t grp = g0; grp - q < groups; grp += 4u * ROWS_WARPS) {
 #pragma unroll
-    for (int p = 0; p < D; ++p) fetch(g0 + p * STEP, w[p], s[p], x[p]);
-    for (uint32_t grp = g0; grp - q < groups; grp += D * STEP) {
+        for (int r = 0; r < R; ++r) {
+            uint32_t p0[16], p1[16];
+            const bool one = NV || __all_sync(0xFFFFFFFFu, W::fits(s[2 * r]) && W::fits(s[2 * r + 1]));
+            W::pairs(w[2 * r], s[2 * r], one, p0);
+            W::pairs(w[2 * r + 1], s[2 * r + 1], one, p1);
 #pragma unroll
-        for (int p = 0; p < D; ++p) {
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                uint32_t p0[16], p1[16];
-                const bool one = __all_sync(0xFFFFFFFFu, W::fits(s[p][2 * r]) && W::fits(s[p][2 * r + 1]));
-                W::pairs(w[p][2 * r], s[p][2 * r], one, p0);
-                W::pairs(w[p][2 * r + 1], s[p][2 * r + 1], one, p1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        const uint4 v = x[p][t][i];      // (e0 e1) (e2 e3) (e4 e5) (e6 e7)
-                        mma_16816(acc[r][t], p0[4 * i], p1[4 * i], p0[4 * i + 1], p1[4 * i + 1],
-                                  __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
-                        mma_16816(acc[r][t], p0[4 * i + 2], p1[4 * i + 2], p0[4 * i + 3], p1[4 * i + 3],
-                                  __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-                    }
+                for (int t = 0; t < MT; ++t) {
+                    const uint4 v = x[t][i];                     // (e0 e1) (e2 e3) (e4 e5) (e6 e7)
+                    mma_16816(acc[r][t], p0[4 * i], p1[4 * i], p0[4 * i + 1], p1[4 * i + 1],
+                              __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
+                    mma_16816(acc[r][t], p0[4 * i + 2], p1[4 * i + 2], p0[4 * i + 3], p1[4 * i + 3],
+                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 }
             }
-            fetch(grp + (D + p) * STEP, w[p], s[p], x[p]);
         }
+        if (grp - q + 4u * ROWS_WARPS < groups) fetch(grp + 4u * ROWS_WARPS);
     }
 
 #pragma unroll
@@ -873,20 +869,22 @@ cudaError_t run_mma(const LinearArgs& a, cudaStream_t st)
     return pl.pair ? run_plan<OP, FMT, NV, true>(a, pl, sms, st) : run_plan<OP, FMT, NV, false>(a, pl, sms, st);
 }
 
-template <bool NV, int R>
+template <bool NV, int R, int MT>
 cudaError_t run_rows(const LinearArgs& a, cudaStream_t st)
 {
-    const unsigned grid = ceil_div(a.ni, 16u * R);
-    return a.nj <= 8 ? launch_pdl(k_linear_rows<NV, R, 1, 2>, grid, 32 * ROWS_WARPS, 0, st, a)
-                     : launch_pdl(k_linear_rows<NV, R, 2, 1>, grid, 32 * ROWS_WARPS, 0, st, a);
+    return launch_pdl(k_linear_rows<NV, R, MT>, ceil_div(a.ni, 16u * R), 32 * ROWS_WARPS, 0, st, a);
 }
 
 template <bool NV>
 cudaError_t run_forward(const LinearArgs& a, cudaStream_t st)
 {
     if (a.nj > 16) return run_mma<LIN_FORWARD, BQ_FP4_E2M1, NV>(a, st);
-    // two CTAs per SM at 32 rows each, else 16 rows so that every SM has work
-    return ceil_div(a.ni, 32u) >= 2u * (uint32_t)device_sm_count() ? run_rows<NV, 2>(a, st) : run_rows<NV, 1>(a, st);
+    // 32 rows share each read of x, 16 have more loads under way: 32 for more than 4 tokens
+    // where that leaves two CTAs per SM (11008 x 4096, us: 1 token 10.0 with 16 rows, 11.5 with
+    // 32; 8 tokens 13.8 and 12.0)
+    const bool two = a.nj > 4 && ceil_div(a.ni, 32u) >= 2u * (uint32_t)device_sm_count();
+    if (a.nj <= 8) return two ? run_rows<NV, 2, 1>(a, st) : run_rows<NV, 1, 1>(a, st);
+    return run_rows<NV, 1, 2>(a, st);
 }
 
 }  // namespace
