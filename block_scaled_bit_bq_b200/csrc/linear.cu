@@ -58,16 +58,10 @@ __device__ __forceinline__ uint32_t ldg_u32(const uint8_t* p)
     return v;
 }
 
-// The scale bytes of 32 codes of a row (32-code group grp): one MX byte, or two NV bytes.
-template <bool NV>
-__device__ __forceinline__ uint32_t load_scale(const LinearArgs& a, uint32_t row, uint32_t grp)
-{
-    return NV ? ldg_u16(a.scales + scale_offset(a, row, 2 * grp)) : ldg_u8(a.scales + scale_offset(a, row, grp));
-}
-
-// The same of two 32-code groups, grp (even) and grp + 1, the second where it exists: in one
-// load where a row's scales start on a multiple of its size (wide). The loaded words are taken
-// apart only where they are used (pair_scale): doing so here would wait for them.
+// The scale bytes of two 32-code groups of a row (one MX byte or two NV bytes each), at p: of an
+// even group and of the one after it, the second where it exists. In one load where a row's
+// scales start on a multiple of its size (wide). The loaded words are taken apart only where
+// they are used (pair_scale): doing so here would wait for them.
 template <bool NV>
 __device__ __forceinline__ void load_scale_pair(const uint8_t* p, bool wide, bool second, uint32_t (&s)[2])
 {
@@ -95,19 +89,43 @@ __device__ __forceinline__ void store_out(const LinearArgs& a, size_t o, float v
     else reinterpret_cast<float*>(a.out)[o] = v;
 }
 
-// n (at most 32) values of one column i of out, rows apart, the first at element o; times sc.
-__device__ __forceinline__ void store_column(const LinearArgs& a, size_t o, uint32_t n, const uint32_t (&v)[32], float sc)
+// n (at most 32) rows of out from row j on, 32 columns (i0 + lane) by a warp, lane l holding
+// column i0 + l: v[e] is row j + e. Times sc, rounded to out's type. As bf16 with rows of whole
+// groups of four columns, lanes swap 4 x 4 blocks first and store 8 bytes of four rows at a
+// time (a quarter of the stores).
+__device__ __forceinline__ void store_rows(const LinearArgs& a, uint32_t j, uint32_t i0, uint32_t lane, uint32_t n,
+                                           const uint32_t (&v)[32], float sc)
 {
-    if (a.out_bf16) {
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
+    const uint32_t i = i0 + lane;
+    if (!a.out_bf16) {
+        float* p = reinterpret_cast<float*>(a.out) + (size_t)j * a.ni + i;
 #pragma unroll
         for (uint32_t e = 0; e < 32; ++e, p += a.ni)
-            if (e < n) *p = __float2bfloat16_rn(__fmul_rn(__uint_as_float(v[e]), sc));
+            if (e < n && i < a.ni) *p = __fmul_rn(__uint_as_float(v[e]), sc);
+    } else if (a.ni % 4u != 0) {
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)j * a.ni + i;
+#pragma unroll
+        for (uint32_t e = 0; e < 32; ++e, p += a.ni)
+            if (e < n && i < a.ni) *p = __float2bfloat16_rn(__fmul_rn(__uint_as_float(v[e]), sc));
     } else {
-        float* p = reinterpret_cast<float*>(a.out) + o;
+        const uint32_t i4 = i & ~3u, dr = ((lane & 2u) ? 2u : 0u) + (lane & 1u);     // this lane's row of four
+        const uint32_t sel = (lane & 1u) ? 0x3276u : 0x5410u;
+        const bool up = (lane & 2u) != 0u;
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)(j + dr) * a.ni + i4;
 #pragma unroll
-        for (uint32_t e = 0; e < 32; ++e, p += a.ni)
-            if (e < n) *p = __fmul_rn(__uint_as_float(v[e]), sc);
+        for (uint32_t e = 0; e < 32; e += 4, p += (size_t)4 * a.ni) {
+            uint32_t r[2];
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {       // rows e + 2 h and + 1: a pair of columns per lane, of one row
+                const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(__uint_as_float(v[e + 2 * h]), sc),
+                                                               __fmul_rn(__uint_as_float(v[e + 2 * h + 1]), sc));
+                const uint32_t own = *reinterpret_cast<const uint32_t*>(&b);
+                r[h] = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);
+            }
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? r[0] : r[1], 2);
+            const uint32_t w[2] = {up ? got : r[0], up ? r[1] : got};
+            if (e + dr < n && i4 < a.ni) st_v2(p, w);
+        }
     }
 }
 
@@ -240,7 +258,8 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 }
 
 // ---------------------------------------------------------------------------
-// Tensor cores. out^T in tiles of 128 (i) x bt (j); 64 steps of the contraction per stage:
+// Tensor cores. out^T in tiles of 128 (i) x bt (j), the contraction in parts of 64 steps, one
+// or two to a stage of the ring:
 //   A: Q widened to bf16, 128 i x 64 c (16 KB), by the widening warps: four groups of four
 //      warps take the parts (64 steps) in turn, a thread 64 codes of one stored row. The codes
 //      come through a ring of their own, 16 KB chunks of four parts (two of 8-bit codes) by
@@ -253,9 +272,9 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 // LIN_GRAD_WEIGHT) it is MN-major: chunks of 64 i (or j) x 64 c, a row of 128 bytes per c, and
 // the tensor cores transpose it. Either way a thread's 64 values are one row of 128 bytes.
 //
-// Warp 0 issues the copies of X, warp 22 those of the codes, warp 1 the MMAs (4 of 16 steps a
+// Warp 0 issues the copies of X, warp 26 those of the codes, warp 1 the MMAs (4 of 16 steps a
 // part, fp32 accumulator in tensor memory, two of them so that a tile's epilogue overlaps the
-// next tile), warps 2-17 widen, warps 18-21 write the accumulator out. A CTA per SM, persistent
+// next tile), warps 2-17 widen, warps 18-25 write the accumulator out. A CTA per SM, persistent
 // over the tiles. Large products run on pairs of CTAs (PAIR): a tile is 256 i x 256 j, each CTA
 // of a pair widens its own 128 i and copies its own 128 j, and the first one issues MMAs that
 // read both (half the shared memory and copies of X per MMA of a lone CTA). With fewer tiles
@@ -266,7 +285,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 
 constexpr uint32_t WIDEN_GROUPS = 4, GROUP_WARPS = 4, GROUP_THREADS = 32 * GROUP_WARPS;
 constexpr uint32_t WIDEN_WARPS = WIDEN_GROUPS * GROUP_WARPS;
-constexpr uint32_t EPI_WARP = 2 + WIDEN_WARPS, CODES_WARP = EPI_WARP + 4;
+constexpr uint32_t EPI_WARP = 2 + WIDEN_WARPS, EPI_WARPS = 8, CODES_WARP = EPI_WARP + EPI_WARPS;
 constexpr int MMA_THREADS = 32 * (CODES_WARP + 1);
 constexpr int MAX_STAGES = 8, MAX_CHUNKS = 8;
 constexpr uint32_t CHUNK_BYTES = 16384;
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     // this CTA's (pair's) tiles and its part of the contraction
     const uint32_t share = PAIR ? 2u : pl.split;
     const uint32_t first = share > 1 ? blockIdx.x / share : blockIdx.x;
-    const uint32_t step = PAIR ? gridDim.x / 2u : pl.split > 1 ? pl.tiles : gridDim.x;
+    const uint32_t step = PAIR ? gridDim.x / 2u : (pl.split > 1 ? pl.tiles : gridDim.x);
     const uint32_t krank = PAIR ? 0u : rank;
     const uint32_t p0 = 4u * (uint32_t)((uint64_t)pl.blocks * krank / pl.split);          // first part
     const uint32_t kts = 4u * (uint32_t)((uint64_t)pl.blocks * (krank + 1) / pl.split) - p0;   // parts
@@ -441,7 +460,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&acc_full[b]), 1);
-            mbar_init(smem_addr(&acc_empty[b]), PAIR ? 8 : 4);
+            mbar_init(smem_addr(&acc_empty[b]), PAIR ? 2u * EPI_WARPS : EPI_WARPS);
         }
         mbar_init(smem_addr(&done_bar), 1);
         abort_flag = 0;
@@ -675,8 +694,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 (void)mbar_wait(smem_addr(&code_full[j]), (j < c ? round : round - 1) & 1u);
         }
     } else {
-        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, i.e. 32 i ----
-        const uint32_t q = warp & 3u, il = q * 32u + lane;
+        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, i.e. 32 i, and
+        // every second 32 columns ----
+        const uint32_t q = warp & 3u, il = q * 32u + lane, half = (warp - EPI_WARP) >> 2;
         const float sc = out_scale<NV>(a);
         uint32_t n = 0;
         for (uint32_t t = first; t < pl.tiles; t += step, ++n) {
@@ -685,9 +705,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
             ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t i = tile_i0(t) + il, j0 = tile_j0(t);
+            const uint32_t i0 = tile_i0(t) + q * 32u, j0 = tile_j0(t);
             const uint32_t cols = min(tile_j, a.nj - j0);
-            for (uint32_t c0 = 0; c0 < cols; c0 += 32u) {
+            for (uint32_t c0 = half * 32u; c0 < cols; c0 += 64u) {
                 uint32_t v[32];
                 tmem_ld32(tmem + b * ACC_COLS + ((q * 32u) << 16) + c0, v);
                 if (pl.split > 1) {
@@ -696,8 +716,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                     for (uint32_t e = 0; e < 32; ++e)
                         if (c0 + e < bt)
                             asm volatile("st.shared.b32 [%0], %1;" :: "r"(base + ((c0 + e) * 128u + il) * 4u), "r"(v[e]) : "memory");
-                } else if (i < a.ni) {
-                    store_column(a, (size_t)(j0 + c0) * a.ni + i, min(32u, cols - c0), v, sc);
+                } else {
+                    store_rows(a, j0 + c0, i0, lane, min(32u, cols - c0), v, sc);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -796,10 +816,12 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
         const uint64_t cost = ((tiles + sms - 1) / sms) * std::max(bt, 128u);
         if (cost < best) { best = cost; p.bt = bt; }
     }
-    // pairs of CTAs where their larger tiles fill the SMs as well
+    // pairs of CTAs (a part of a tile costs them no more than a lone CTA's, see above) where they
+    // take no more rounds: a little more from one tile for each pair of SMs on, no more from two
+    // thirds of that
     const uint64_t pair_tiles = (uint64_t)ceil_div(a.ni, 256u) * ceil_div(a.nj, 256u);
     const uint64_t pair_cost = ((pair_tiles + sms / 2 - 1) / (sms / 2)) * 256u;
-    p.pair = pair_tiles >= sms / 2 && pair_cost * 4 <= best * 5 ? 1u : 0u;
+    p.pair = pair_tiles * 3 >= sms && pair_cost * 4 <= best * (pair_tiles >= sms / 2 ? 5u : 4u) ? 1u : 0u;
     if (p.pair) {
         p.bt = 128;
         p.tiles_i = ceil_div(a.ni, 256u);
@@ -813,7 +835,7 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     // two chunks of codes at least, up to four stages, then more chunks: with narrow tiles the
     // codes are most of what is read, and their ring keeps the memory busy
     const uint32_t room = SMEM_ROOM, stage = plan_stage_bytes(p);
-    p.stages = std::min(p.pair ? 6u : 4u, (room - 2u * CHUNK_BYTES) / stage);          // times subs >= 4 parts (see there)
+    p.stages = std::min(4u, (room - 2u * CHUNK_BYTES) / stage);          // four parts or more
     p.chunks = std::min<uint32_t>(MAX_CHUNKS, (room - p.stages * stage) / CHUNK_BYTES) & ~1u;
     return p;
 }
