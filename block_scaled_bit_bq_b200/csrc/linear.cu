@@ -138,6 +138,10 @@ __device__ __forceinline__ void store_rows(const LinearArgs& a, uint32_t j, uint
 // 8 of each 16 (16 bytes each) and the 32 values q of token g, and takes the columns in the
 // order in which widening leaves them: an mma.sync adds up 16 columns in any order as long as
 // both operands use the same one. The warps' sums meet in shared memory, in warp order.
+//
+// The weight's bytes set the floor; widening them (half the ALU's rate) with few warps to hide
+// the loads behind is what bounds it above that: 8 tokens x 28672 x 8192 under NV in 46-50 us,
+// 2.7-2.9 TB/s of 133 MB (the same loads alone: 29 us).
 // ---------------------------------------------------------------------------
 
 constexpr int ROWS_WARPS = 8;
@@ -281,6 +285,10 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 // than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
 // through distributed shared memory, in rank order: no workspace, and the same sums every time.
 // Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
+//
+// 4096 tokens x 11008 x 4096: 272 us forward, 269 input gradient, 301 weight gradient (1.36,
+// 1.37 and 1.23 PFLOP/s; tensor pipe active 66-75 %, the widening warps' ALU 47-52 %). With few
+// tokens the hand-over of a part (about 0.35 us whatever the tile's width) bounds it.
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t WIDEN_GROUPS = 4, GROUP_WARPS = 4, GROUP_THREADS = 32 * GROUP_WARPS;
@@ -300,7 +308,7 @@ struct MmaPlan {
     uint32_t subs;          // 64-step parts of a stage: 1 or 2
     uint32_t stages;        // of the ring
     uint32_t chunks;        // of the code ring
-    uint32_t tiles_i, tiles_j, tiles;
+    uint32_t tiles_i, tiles;    // tiles of i, and in all (i by i)
     uint32_t blocks;        // of the contraction: 256 steps, four parts, each
     uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
     uint32_t pair;          // 1: tiles of 256 x 256 on pairs of CTAs (bt 128 each)
@@ -401,17 +409,6 @@ __device__ __forceinline__ float4 sum_cluster(uint32_t addr)
     return v;
 }
 
-// Tile t: (tile of i, tile of j). Groups of 8 tiles of j, i by i, j fastest: the CTAs at work
-// at a time then read several tiles of X (with one, all of them asked the L2 for the same lines
-// at once, and the copies of X alone took as long as everything else: 525 of 487 us for 4096
-// tokens x 11008 x 4096) and few of Q.
-__device__ __forceinline__ uint2 tile_at(const MmaPlan& p, uint32_t t)
-{
-    const uint32_t per_group = 8u * p.tiles_i, grp = t / per_group, rem = t - grp * per_group;
-    const uint32_t j0 = grp * 8u, w = min(8u, p.tiles_j - j0);
-    return make_uint2(rem / w, j0 + rem % w);
-}
-
 template <int OP, int FMT, bool NV, bool PAIR>
 __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_constant__ CUtensorMap xmap,
                                                              const __grid_constant__ CUtensorMap qmap,
@@ -445,8 +442,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     // but nothing is copied, widened or multiplied for them
     auto live = [&](uint32_t part) { return (uint64_t)part * 64u < a.nc; };
     // first i of a tile for this CTA, and first j of the tile
-    auto tile_i0 = [&](uint32_t t) { return tile_at(pl, t).x * (PAIR ? 256u : 128u) + (PAIR ? rank * 128u : 0u); };
-    auto tile_j0 = [&](uint32_t t) { return tile_at(pl, t).y * tile_j; };
+    auto tile_i0 = [&](uint32_t t) { return t % pl.tiles_i * (PAIR ? 256u : 128u) + (PAIR ? rank * 128u : 0u); };
+    auto tile_j0 = [&](uint32_t t) { return t / pl.tiles_i * tile_j; };
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < NS; ++s) {
@@ -639,7 +636,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 const uint32_t s0 = pair_scale<NV>(sc[0], wide, 0), s1 = pair_scale<NV>(sc[0], wide, 1);
                 sc[0][0] = sc[1][0];
                 sc[0][1] = sc[1][1];
-                const bool one = __all_sync(0xFFFFFFFFu, W::fits(s0) && W::fits(s1));
+                const bool one = __all_sync(0xFFFFFFFFu, W::fits(s0) && W::fits(s1) && W::numbers(w[0]) && W::numbers(w[1]));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t v[W::WORDS * W::RAW];
@@ -826,8 +823,7 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
         p.bt = 128;
         p.tiles_i = ceil_div(a.ni, 256u);
     }
-    p.tiles_j = ceil_div(a.nj, p.pair ? 256u : p.bt);
-    p.tiles = p.tiles_i * p.tiles_j;
+    p.tiles = p.tiles_i * ceil_div(a.nj, p.pair ? 256u : p.bt);
     p.subs = p.bt > 128u ? 1u : 2u;
     p.blocks = ceil_div(a.nc, 256u);
     p.split = 1;

@@ -70,9 +70,26 @@ struct Widen {
     // Whether a block's scale and the missing factor are one multiplier.
     static __device__ __forceinline__ bool fits(uint32_t scale) { return OFF == 0 || NV || scale <= LIMIT; }
 
+    // FP8 codes that are no numbers (E4M3: S.1111.111, E5M2: exponent 31) come from NaN in what
+    // was quantized. Whether w has none: the addition flips bit 7 of such a byte, and of no other
+    // below the first one. (Looking costs the weight gradient 6 % at 4096 tokens x 11008 x 4096,
+    // 285 to 301 us, however it is spelt, and 10 % when it is done after the widening.)
+    static constexpr bool HAS_NAN = FMT == BQ_FP8_E4M3 || FMT == BQ_FP8_E5M2;
+    static constexpr uint32_t BEYOND = FMT == BQ_FP8_E4M3 ? 0x01010101u : 0x04040404u;
+
+    static __device__ __forceinline__ bool numbers(const uint32_t (&w)[WORDS])
+    {
+        uint32_t any = 0;
+        if constexpr (HAS_NAN) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) any |= (w[i] + BEYOND) ^ w[i];
+        }
+        return (any & 0x80808080u) == 0u;
+    }
+
     // The raw pairs of all words times their blocks' scales. scale: the MX byte, or the two NV
-    // bytes (first block's low). one: fits(scale), or false for any scale (a warp decides for
-    // all its lanes).
+    // bytes (first block's low). one: fits(scale) and numbers(w), or false for any (a warp decides
+    // for all its lanes).
     static __device__ __forceinline__ void pairs(const uint32_t (&w)[WORDS], uint32_t scale, bool one,
                                                  uint32_t (&p)[WORDS * RAW])
     {
@@ -103,6 +120,13 @@ struct Widen {
                 raw(w[i], r);
 #pragma unroll
                 for (int j = 0; j < RAW; ++j) p[i * RAW + j] = bf2_mul(bf2_mul(r[j], off), e);
+                if constexpr (HAS_NAN) {
+                    // bit 7 of a byte: no number, NaN. All exponent bits make the value Inf or NaN
+                    constexpr uint32_t above_inf = FMT == BQ_FP8_E4M3 ? 0x01010101u : 0x03030303u;
+                    const uint32_t mag = w[i] & 0x7F7F7F7Fu, s = mag + BEYOND, n = mag + above_inf;
+                    p[i * RAW] |= (s & 0x00800080u) * 0xFFu | (n & 0x00800080u) >> 1;
+                    p[i * RAW + 1] |= ((s >> 8) & 0x00800080u) * 0xFFu | ((n >> 8) & 0x00800080u) >> 1;
+                }
             }
         }
     }

@@ -398,8 +398,8 @@ bq_status bq_gemm(const void* a_codes, const void* a_scales, const float* a_tens
  * (else BQ_ERR_SHAPE); m, n, k, ld < 2^31, m * k, m * n and n * k at most 2^36 - 2048.
  * m == 0 (n == 0): an output without elements is left alone, and a gradient that sums over
  * no tokens (no outputs) is set to zero. Codes: 32-byte aligned; scales and the tensor scale
- * 4-byte aligned (BQ_ERR_ALIGNMENT). Non-finite x or dy follow IEEE arithmetic. No workspace;
- * enqueued on stream; every wait in the kernels is bounded (bq_wait_timeouts counts those that
+ * 4-byte aligned (BQ_ERR_ALIGNMENT). Non-finite x or dy, and NaN or Inf
+ * codes of an FP8 X, follow IEEE arithmetic. No workspace; enqueued on stream; every wait in the kernels is bounded (bq_wait_timeouts counts those that
  * gave up).
  */
 bq_status bq_linear(const void* x, int32_t x_dtype, int64_t ldx,

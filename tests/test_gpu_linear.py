@@ -244,6 +244,37 @@ def test_non_finite_values_stay_in_their_row(m):
     _close(y[keep], _f64(x[keep]), w.T, torch.float32, 96)
 
 
+# every code, those of NaN and Inf among them; sums of few tokens, so that most stay finite
+@pytest.mark.parametrize("fmt,dt", [("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)])
+@pytest.mark.parametrize("m,n", [(3, 72), (2, 600)])
+def test_grad_weight_codes_that_are_no_numbers(fmt, dt, m, n):
+    k = 1024
+    q, _ = _quantized(_acts(m, k, 993), Scheme(fmt, "mx"))
+    q.codes.copy_(torch.from_numpy(np.random.default_rng(994).permutation(np.arange(m * k) % 256).astype(np.uint8))
+                  .view(q.codes.shape))
+    q.scales.fill_(125)
+    dy = torch.where(_acts(m, n, 995) < 0, -1.5, 0.75).to(torch.bfloat16)
+    got = bq.linear_grad_weight(dy.cuda(), q, torch.float32).cpu().double()
+    want = dy.double().T @ (q.codes.cpu().view(m, k).view(dt).double() * 0.25)
+    assert torch.isnan(want).any() and torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], want[inf])
+    fin = torch.isfinite(want)
+    mags = dy.double().abs().T @ torch.nan_to_num(q.codes.cpu().view(m, k).view(dt).double().abs() * 0.25, 0.0, 0.0)
+    assert ((got - want).abs()[fin] <= ((m / 8 + 32) * 2.0 ** -23 * mags + 2.0 ** -24 * want.abs())[fin]).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_grad_weight_of_an_input_with_nan(fmt):
+    m, n, k = 70, 136, 96
+    x = _acts(m, k, 996)
+    x[66, 40] = float("nan")
+    q = bq.quantize(x.cuda(), Scheme(fmt, "mx"), stats=False)
+    dw = bq.linear_grad_weight(torch.ones(m, n, dtype=torch.bfloat16, device="cuda"), q, torch.float32).cpu()
+    assert torch.isnan(dw[:, 40]).all()
+    assert torch.isfinite(dw[:, :32]).all() and torch.isfinite(dw[:, 64:]).all()
+
+
 # the same bits from call to call, on another stream, and from a captured graph with new inputs
 @pytest.mark.parametrize("m", [1, 7, 24, 300])
 def test_repeats_streams_and_graphs(m):
