@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 // Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
 //
 // 4096 tokens x 11008 x 4096: 272 us forward, 269 input gradient, 301 weight gradient (1.36,
-// 1.37 and 1.23 PFLOP/s; tensor pipe active 66-75 %, the widening warps' ALU 47-52 %). With few
+// 1.37 and 1.23 PFLOP/s; tensor pipe active 61-74 %, the widening warps' ALU 45-50 %). With few
 // tokens the hand-over of a part (about 0.35 us whatever the tile's width) bounds it.
 // ---------------------------------------------------------------------------
 
