@@ -339,6 +339,13 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, 
                      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+template <bool PAIR>
+__device__ __forceinline__ void load_x(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, x, y);
+    else tma_load_2d(dst, map, bar, x, y);
+}
+
 // Commit of the MMAs so far: an arrival on bar, in a pair on that barrier of both CTAs.
 template <bool PAIR>
 __device__ __forceinline__ void tc_commit_all(uint32_t bar)
@@ -350,15 +357,22 @@ __device__ __forceinline__ void tc_commit_all(uint32_t bar)
         tc_commit(bar);
 }
 
-// Arrival on the first CTA's barrier (bar: its address in this CTA). Without a cluster-scope
-// release, which takes about 900 cycles (a pair's stages then took 1340 instead of 700): what
-// it hands over lies in this CTA's own shared memory and was made visible here before, by the
-// copies' completion or by the writers' proxy fence and arrivals, and is read by this SM's
-// tensor core.
+// Arrivals on the first CTA's barrier (bar: its address in this CTA), for its thread that waits
+// there to let MMAs go that read, or write over, what this CTA holds. Of shared memory written
+// before (its waits: ACQ_SHARED); a release of everything, global memory too, takes about 900
+// cycles, and 4096 tokens x 11008 x 4096 forward 316 us with it.
+__device__ __forceinline__ void mbar_arrive_first_shared(uint32_t bar)
+{
+    fence_release_shared();
+    asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %0, 0;\n"
+                 "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [p];\n}" :: "r"(bar) : "memory");
+}
+
+// Of everything before, accumulator reads among it (its waits: ACQ_CLUSTER): once a tile.
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
 {
     asm volatile("{\n.reg .b32 p;\nmapa.shared::cluster.u32 p, %0, 0;\n"
-                 "mbarrier.arrive.shared::cluster.b64 _, [p];\n}" :: "r"(bar) : "memory");
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [p];\n}" :: "r"(bar) : "memory");
 }
 
 // One lane of a converged warp.
@@ -447,7 +461,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < NS; ++s) {
-            // the widening warps, the copies, and the other CTA of the pair
+            // the widening warps and the warp that issues the copies; in a pair the first CTA's
+            // barrier is the stage's: both CTAs' copies complete on it, and the second CTA arrives
+            // there once its own is complete
             mbar_init(smem_addr(&full[s]), subs * GROUP_WARPS + 1u + (PAIR && rank == 0 ? 1u : 0u));
             mbar_init(smem_addr(&empty[s]), 1);
         }
@@ -496,14 +512,19 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                     const uint32_t fb = smem_addr(&full[s]);
                     uint32_t dst = base + s * stage_bytes + A_BYTES, part = p0 + kk * subs;
                     const uint32_t n_live = live(part) ? (subs == 2 && live(part + 1) ? 2u : 1u) : 0u;
-                    mbar_arrive_expect_tx(fb, n_live * b_bytes);
+                    // a pair's MMAs read both CTAs' X on either SM: both CTAs' bytes are awaited on the
+                    // first one's barrier (this slot's earlier use is over there too: its MMAs freed the
+                    // slot here). The second CTA's warp arrives on its own all the same, so that it
+                    // cannot fall behind by a use of a slot, which a wait by parity would not tell
+                    if (PAIR && rank != 0) mbar_arrive(fb);
+                    else mbar_arrive_expect_tx(fb, (PAIR ? 2u : 1u) * n_live * b_bytes);
                     for (uint32_t u = 0; u < n_live; ++u, ++part, dst += sub_bytes) {
                         const int c = (int)(part * 64u);
                         if (OP == LIN_GRAD_WEIGHT) {
                             for (uint32_t x = 0; x < bt / 64u; ++x)
-                                tma_load_2d(dst + x * 8192u, &xmap, fb, j0 + (int)(64u * x), c);
+                                load_x<PAIR>(dst + x * 8192u, &xmap, fb, j0 + (int)(64u * x), c);
                         } else {
-                            tma_load_2d(dst, &xmap, fb, c, j0);
+                            load_x<PAIR>(dst, &xmap, fb, c, j0);
                         }
                     }
                 }
@@ -513,7 +534,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         }
         // the copies in flight (at most one stage a slot) land before the CTA can exit: after an
         // abort the full barriers may stay short of the widening warps' arrivals, so the wait
-        // (bounded) is for their time only
+        // (bounded) is for their time only (in a pair the first CTA waits for both: neither
+        // leaves before the other)
         if (abort_flag) {
             for (uint32_t j = 0; j < NS && (round > 0 || j < s); ++j)
                 (void)mbar_wait(smem_addr(&full[j]), (j < s ? round : round - 1) & 1u);
@@ -528,12 +550,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint64_t bd0 = OP == LIN_GRAD_WEIGHT ? mn_desc(base + A_BYTES) : operand_desc(base + A_BYTES);
         uint32_t s = 0, par = 0, i = 0;
         if (PAIR && rank != 0) {
-            // the second CTA of a pair only says when its half of a stage is there
+            // the second CTA of a pair only says when its codes of a stage are widened
             for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
                     if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
                     if (abort_flag) break;
-                    if (leader) mbar_arrive_first(smem_addr(&full[s]));
+                    if (leader) mbar_arrive_first_shared(smem_addr(&full[s]));
                     __syncwarp();
                     if (++s == NS) { s = 0; par ^= 1u; }
                 }
@@ -541,12 +563,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         } else {
             for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
                 const uint32_t b = i & 1u;
-                if (i >= 2 && !mbar_wait_ring(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
+                if (i >= 2 && !mbar_wait_ring<PAIR ? ACQ_CLUSTER : ACQ_CTA>(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + b * ACC_COLS;
                 uint32_t acc = 0;
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
-                    if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
+                    if (!mbar_wait_ring<PAIR ? ACQ_SHARED : ACQ_CTA>(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     for (uint32_t u = 0; u < subs; ++u) {
                         const uint64_t so = (s * stage_bytes + u * sub_bytes) >> 4, ad = ad0 + so, bd = bd0 + so;
@@ -698,7 +720,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         uint32_t n = 0;
         for (uint32_t t = first; t < pl.tiles; t += step, ++n) {
             const uint32_t b = n & 1u;
-            bool ok = mbar_wait_ring(smem_addr(&acc_full[b]), (n / 2) & 1u);
+            bool ok = mbar_wait_ring<PAIR ? ACQ_CLUSTER : ACQ_CTA>(smem_addr(&acc_full[b]), (n / 2) & 1u);
             ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -49,12 +49,63 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y) : "memory");
 }
 
+// tma_load_2d in a pair of CTAs (cta_group::2): into this CTA's shared memory, its bytes
+// completed on the first CTA's barrier (bar: that barrier's address in this CTA).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "{\n.reg .b32 b;\nmapa.shared::cluster.u32 b, %2, 0;\n"
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%3, %4}], [b];\n}"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+
 // Box {x, y, z} of a 3-D tensor map (same rules as tma_load_2d).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// What a wait makes visible to the waiting thread: ACQ_CTA what threads of its CTA wrote before
+// they arrived (and copies that completed on the barrier); ACQ_CLUSTER what threads of another
+// CTA of the cluster did before an arrival released at cluster scope; ACQ_SHARED the same for
+// shared memory alone, after fence_release_shared and a relaxed arrival (without the trip to L2
+// that ordering global memory takes).
+enum { ACQ_CTA = 0, ACQ_CLUSTER = 1, ACQ_SHARED = 2 };
+
+// One try at the phase with the given parity, which may sleep up to hint_ns in hardware until it
+// completes. ACQ_SHARED: relaxed, fence_acquire_shared is to follow.
+template <int ACQ>
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t hint_ns)
+{
+    uint32_t ok;
+    if constexpr (ACQ == ACQ_CTA)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(hint_ns) : "memory");
+    else if constexpr (ACQ == ACQ_CLUSTER)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(hint_ns) : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(hint_ns) : "memory");
+    return ok != 0u;
+}
+
+__device__ __forceinline__ void fence_acquire_shared()
+{
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
+__device__ __forceinline__ void fence_release_shared()
+{
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
@@ -91,16 +142,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 // mbar_wait for stage rings, whose waits are short and many: each try may sleep in hardware
 // until the phase completes (a hint of up to a millisecond) instead of polling, and the clock
 // is read only after tries have failed (reading it takes longer than most waits last).
+template <int ACQ = ACQ_CTA>
 __device__ __forceinline__ bool mbar_wait_ring(uint32_t bar, uint32_t parity)
 {
-    for (int i = 0; i < 64; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
-        if (ok) return true;
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try<ACQ>(bar, parity, 1000000u);
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+        do ok = mbar_try<ACQ>(bar, parity, 1000000u);
+        while (!ok && global_ns() - t0 <= WAIT_LIMIT_NS);
     }
-    return mbar_wait(bar, parity);
+    if constexpr (ACQ == ACQ_SHARED) fence_acquire_shared();
+    return ok;
 }
 
 // 16-byte shared-memory accesses.
