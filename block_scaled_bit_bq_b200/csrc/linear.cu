@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 // read both (half the shared memory and copies of X per MMA of a lone CTA). With fewer tiles
 // than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
 // through distributed shared memory, in rank order: no workspace, and the same sums every time.
-// Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts).
+// Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts), the
+// epilogue's for an accumulator after a second in which no stage was done.
 //
 // 4096 tokens x 11008 x 4096: 272 us forward, 269 input gradient, 301 weight gradient (1.36,
 // 1.37 and 1.23 PFLOP/s; tensor pipe active 61-74 %, the widening warps' ALU 45-50 %). With few
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         code_empty[MAX_CHUNKS], acc_full[2], acc_empty[2], done_bar;
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
+    __shared__ volatile uint32_t stages_done;        // of the MMA warp (of a pair's second CTA: handed over)
     // (from lane 0, so that the compiler sees the warps' roles as uniform branches)
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     const uint32_t base = (smem_addr(linear_smem) + 1023u) & ~1023u;
@@ -477,6 +479,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         }
         mbar_init(smem_addr(&done_bar), 1);
         abort_flag = 0;
+        stages_done = 0;
         fence_mbar_init();
     }
     __syncwarp();
@@ -548,14 +551,17 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint32_t idesc = mma_desc<OP>(PAIR ? 256u : 128u, tile_j);
         const uint64_t ad0 = OP == LIN_FORWARD ? operand_desc(base) : mn_desc(base);
         const uint64_t bd0 = OP == LIN_GRAD_WEIGHT ? mn_desc(base + A_BYTES) : operand_desc(base + A_BYTES);
-        uint32_t s = 0, par = 0, i = 0;
+        uint32_t s = 0, par = 0, i = 0, stage = 0;
         if (PAIR && rank != 0) {
             // the second CTA of a pair only says when its codes of a stage are widened
             for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
                     if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
                     if (abort_flag) break;
-                    if (leader) mbar_arrive_first_shared(smem_addr(&full[s]));
+                    if (leader) {
+                        mbar_arrive_first_shared(smem_addr(&full[s]));
+                        stages_done = ++stage;
+                    }
                     __syncwarp();
                     if (++s == NS) { s = 0; par ^= 1u; }
                 }
@@ -579,7 +585,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                         }
                         acc = 1;
                     }
-                    if (leader) tc_commit_all<PAIR>(smem_addr(&empty[s]));
+                    if (leader) {
+                        tc_commit_all<PAIR>(smem_addr(&empty[s]));
+                        stages_done = ++stage;
+                    }
                     __syncwarp();
                     if (++s == NS) { s = 0; par ^= 1u; }
                 }
@@ -720,7 +729,13 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         uint32_t n = 0;
         for (uint32_t t = first; t < pl.tiles; t += step, ++n) {
             const uint32_t b = n & 1u;
-            bool ok = mbar_wait_ring<PAIR ? ACQ_CLUSTER : ACQ_CTA>(smem_addr(&acc_full[b]), (n / 2) & 1u);
+            // a tile's whole contraction may lie before this: the wait goes on as long as stages do
+            bool ok = false;
+            for (uint32_t seen = stages_done, now;; seen = now) {
+                ok = mbar_wait_ring<PAIR ? ACQ_CLUSTER : ACQ_CTA>(smem_addr(&acc_full[b]), (n / 2) & 1u);
+                now = stages_done;
+                if (ok || abort_flag || now == seen) break;
+            }
             ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
