@@ -581,6 +581,25 @@ def _operand(t: torch.Tensor, name: str, rows: int | None, cols: int, dev: torch
     return buf, ld
 
 
+def _handle(q: Quantized, dev: torch.device) -> None:
+    """Refuses a Quantized (a handle can be built by hand) whose buffers an MX or NV kernel would
+    read or write past their end: on another device, not contiguous, or shorter than its scheme
+    and shape ask. (Other schemes are refused by the calls that this serves.)"""
+    s, rows, cols = q.scheme, q.rows, q.cols
+    if s.gran not in ("mx", "nv"):
+        return
+    nb = cols // (32 if s.gran == "mx" else 16)
+    codes, scales, ts = q.codes, q.scales, q.tensor_scale
+    if (codes.device != dev or not codes.is_contiguous() or codes.element_size() != 1
+            or codes.numel() < (rows * cols // 2 if s.fmt in FOUR_BIT else rows * cols)):
+        raise ValueError(f"the codes are not contiguous bytes of a {s.fmt} [{rows}, {cols}] tensor on {dev}")
+    if (scales.device != dev or not scales.is_contiguous() or scales.element_size() != 1
+            or scales.numel() < ((rows + 127) // 128 * 128 if s.layout == "gemm" else rows) * nb):
+        raise ValueError(f"the scales are not contiguous bytes of [{rows}, {nb}] blocks on {dev}")
+    if s.gran == "nv" and ts is not None and (ts.device != dev or ts.dtype is not torch.float32 or ts.numel() < 1):
+        raise ValueError(f"the tensor scale is not fp32 on {dev}")
+
+
 def _out(out: torch.Tensor | None, rows: int, cols: int, dtype, dev: torch.device) -> torch.Tensor:
     if out is None:
         if dtype not in _OUT_DT:
@@ -599,6 +618,7 @@ def linear(x: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tenso
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear(x, w, dtype, out)
+    _handle(w, dev)
     x, ld = _operand(x, "x", None, w.cols, dev, 8)
     m, n = x.shape[0], w.rows
     y = _out(out, m, n, dtype, dev)
@@ -615,6 +635,7 @@ def linear_grad_input(dy: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out:
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear_grad_input(dy, w, dtype, out)
+    _handle(w, dev)
     dy, ld = _operand(dy, "dy", None, w.rows, dev, 8)
     m, k = dy.shape[0], w.cols
     dx = _out(out, m, k, dtype, dev)
@@ -632,6 +653,7 @@ def linear_grad_weight(dy: torch.Tensor, x: Quantized, dtype=torch.float32, out:
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear_grad_weight(dy, x, dtype, out)
+    _handle(x, dev)
     dy, ld = _operand(dy, "dy", x.rows, dy.shape[-1], dev, 8)
     n, k = dy.shape[1], x.cols
     dw = _out(out, n, k, dtype, dev)
@@ -697,8 +719,8 @@ def glu(gate: torch.Tensor, up: torch.Tensor, scheme: Scheme | None = None, act:
         s, g, u = scheme.resolved(), ckpt.gate, ckpt.up
         if g.scheme != s or u.scheme != s or (g.rows, g.cols) != (rows, cols) or (u.rows, u.cols) != (rows, cols):
             raise ValueError("the checkpoint's buffers are of another scheme or shape")
-        if g.codes.device != dev or u.codes.device != dev:
-            raise ValueError(f"the checkpoint's buffers are not on {dev}")
+        _handle(g, dev)
+        _handle(u, dev)
         ckpt.act = act
     _check(_lib().bq_glu(gate.data_ptr(), ldg, up.data_ptr(), ldu, 0, rows, cols, a, h.data_ptr(),
                          ctypes.byref(_c_scheme(s)), g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(),
@@ -715,8 +737,10 @@ def glu_backward(dh: torch.Tensor, ckpt: GluCheckpoint, out=None, stream=None):
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return glu_backward(dh, ckpt, out)
-    if (u.rows, u.cols) != (rows, cols) or u.scheme != g.scheme or u.codes.device != dev:
-        raise ValueError("the two copies must be of one shape and scheme, on one device")
+    if (u.rows, u.cols) != (rows, cols) or u.scheme != g.scheme:
+        raise ValueError("the two copies must be of one shape and scheme")
+    _handle(g, dev)
+    _handle(u, dev)
     dh, ldh = _operand(dh, "dh", rows, cols, dev, 16)
     if out is None:
         dg = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
