@@ -273,6 +273,8 @@ def bq_gemm(a: "Quantized", b: "Quantized", d: torch.Tensor, stream=None) -> Non
 
 def gemm(a: "Quantized", b: "Quantized", dtype=torch.float32, stream=None) -> torch.Tensor:
     """A B^T of two quantized operands (MXFP8 / NVFP4, GEMM-layout scales)."""
+    for q in (a, b):
+        _buffers(q, a.codes.device, q.rows, q.cols)
     d = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
     bq_gemm(a, b, d, stream)
     return d
@@ -413,6 +415,19 @@ def alloc_outputs(scheme: Scheme, rows: int, cols: int, device, stats: bool = Tr
     return Quantized(s, rows, cols, codes, scales, zps, ts, st)
 
 
+def _buffers(q, dev: torch.device, rows: int, cols: int, batch: int = 1) -> None:
+    """Refuses a handle (Quantized, QuantizedBatch) whose buffers do not hold batch tensors of
+    [rows, cols] under its scheme: another device, not contiguous, or too short."""
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    sizes = bq_buffer_sizes(q.scheme, rows, cols)
+    for name, need in zip(("codes", "scales", "zero_points", "tensor_scale"), sizes):
+        t = getattr(q, name, None)
+        if need and t is not None and (t.device != dev or not t.is_contiguous()
+                                       or t.numel() * t.element_size() < need * batch):
+            raise ValueError(f"{name}: expected {need * batch} contiguous bytes on {dev}")
+
+
 @dataclass
 class QuantizedBatch:
     scheme: Scheme
@@ -453,6 +468,8 @@ def quantize_batch(x: torch.Tensor, scheme: Scheme, stats: bool = True, workspac
     x = x.contiguous()
     batch, rows, cols = x.shape
     q = out or alloc_batch_outputs(scheme, batch, rows, cols, x.device, stats)
+    if out is not None:
+        _buffers(q, x.device, rows, cols, batch)
     if stats and workspace is None:
         workspace = new_workspace(x.device)
     bq_quantize_batch(x, q.scheme, q.codes, q.scales, q.zero_points, q.stats if stats else None, workspace, stream)
@@ -468,6 +485,8 @@ def quantize(x: torch.Tensor, scheme: Scheme, stats: bool = True, workspace: tor
     x = x.contiguous()
     rows, cols = x.shape
     q = out or alloc_outputs(scheme, rows, cols, x.device, stats)
+    if out is not None:
+        _buffers(q, x.device, rows, cols)
     if workspace is None and bq_workspace_size(q.scheme, rows, cols, stats) > 0:
         workspace = new_workspace(x.device)
     bq_quantize(x, q.scheme, q.codes, q.scales, q.zero_points, q.tensor_scale, q.stats if stats else None,
@@ -476,6 +495,7 @@ def quantize(x: torch.Tensor, scheme: Scheme, stats: bool = True, workspace: tor
 
 
 def dequantize(q: Quantized, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    _buffers(q, q.codes.device, q.rows, q.cols)
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
     bq_dequantize(q.codes, q.scales, q.zero_points, q.tensor_scale, q.rows, q.cols, q.scheme, out, stream)
@@ -501,6 +521,7 @@ def quantize_rt(x: torch.Tensor, scheme: Scheme, col_scale: torch.Tensor | None 
 
 def dequantize_rt(q: Quantized, col_scale: torch.Tensor | None = None, sign_bits: torch.Tensor | None = None,
                   dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    _buffers(q, q.codes.device, q.rows, q.cols)
     out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
     bq_dequantize_rt(q.codes, q.scales, q.zero_points, q.rows, q.cols, q.scheme, col_scale, sign_bits, out, stream)
     return out
@@ -508,6 +529,7 @@ def dequantize_rt(q: Quantized, col_scale: torch.Tensor | None = None, sign_bits
 
 def qsnr(x: torch.Tensor, q: Quantized, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Standalone QSNR sums (float64[5] on the device; kappa fields zero)."""
+    _buffers(q, x.device, *x.shape)
     st = torch.empty(5, dtype=torch.float64, device=x.device)
     if workspace is None:
         workspace = new_workspace(x.device)

@@ -50,3 +50,24 @@ def test_glu_refuses_bad_checkpoints():
                 bq.glu(g, u, s, ckpt=pair)
             with pytest.raises(ValueError):
                 bq.glu_backward(dh, pair)
+
+
+def test_the_other_calls_refuse_bad_handles():
+    x = torch.randn(128, 256, device="cuda").to(torch.bfloat16)
+    for s in (Scheme("int8_sym", "row"), Scheme("e4m3", "mx", layout="gemm"), Scheme("e2m1", "nv")):
+        q = bq.quantize(x, s, stats=False)
+        want = bq.dequantize(q)
+        for bad in (dataclasses.replace(q, codes=q.codes[:-1]), dataclasses.replace(q, scales=q.scales[:-1]),
+                    dataclasses.replace(q, scales=q.scales.cpu())):
+            calls = [lambda: bq.dequantize(bad), lambda: bq.qsnr(x, bad), lambda: bq.quantize(x, s, stats=False, out=bad)]
+            if s.layout == "gemm":
+                calls += [lambda: bq.gemm(bad, q), lambda: bq.gemm(q, bad)]
+            for call in calls:
+                with pytest.raises(ValueError):
+                    call()
+        with pytest.raises(ValueError):
+            bq.quantize(torch.cat((x, x)), s, stats=False, out=q)
+        assert torch.equal(bq.dequantize(q), want)
+    b = bq.quantize_batch(x.view(2, 64, 256), Scheme("e4m3", "mx"), stats=False)
+    with pytest.raises(ValueError):
+        bq.quantize_batch(x.view(4, 32, 256).repeat(2, 1, 1), b.scheme, stats=False, out=b)

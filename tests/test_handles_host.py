@@ -41,3 +41,56 @@ def test_short_or_strange_buffers_are_refused(s):
             bq._handle(dataclasses.replace(q, **change), CPU)
     with pytest.raises(ValueError):
         bq._handle(q, torch.device("cuda", 0))
+
+
+# the calls that take any scheme: every refusal comes before the library is called
+ANY = [Scheme("int8_sym", "row"), Scheme("uint4_asym", "group", 128, "fp16"), Scheme("e4m3", "tensor"), Scheme("int8_asym", "tile2d"),
+       Scheme("e2m1", "nv"), Scheme("e4m3", "mx", layout="gemm")]
+
+
+class _Elsewhere:
+    """A tensor that says it is on a CUDA device (there is none here)."""
+
+    def __init__(self, t):
+        self.t = t
+
+    device = torch.device("cuda", 0)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def _on_cuda(q):
+    return dataclasses.replace(q, **{n: _Elsewhere(getattr(q, n)) for n in ("codes", "scales", "zero_points", "tensor_scale")
+                                     if getattr(q, n, None) is not None})
+
+
+@pytest.mark.parametrize("s", ANY, ids=lambda s: f"{s.fmt}-{s.gran}")
+def test_buffers_of_any_scheme(s):
+    dev = _Elsewhere.device
+    q = bq.alloc_outputs(s, 130, 256, CPU, stats=False)
+    bq._buffers(_on_cuda(q), dev, 130, 256)
+    for n in ("codes", "scales", "zero_points", "tensor_scale"):
+        t = getattr(q, n)
+        if t is None:
+            continue
+        for short in (t.reshape(-1)[:-1], t.reshape(-1, 1).expand(-1, 2)):
+            with pytest.raises(ValueError):
+                bq._buffers(_on_cuda(dataclasses.replace(q, **{n: short})), dev, 130, 256)
+        with pytest.raises(ValueError):
+            bq._buffers(dataclasses.replace(_on_cuda(q), **{n: t}), dev, 130, 256)
+    with pytest.raises(ValueError):
+        bq._buffers(_on_cuda(q), dev, 386, 256)
+    b = bq.alloc_batch_outputs(s, 3, 130, 256, CPU, stats=False) if s.gran in ("group", "mx") else None
+    if b is not None:
+        bq._buffers(_on_cuda(b), dev, 130, 256, 3)
+        with pytest.raises(ValueError):
+            bq._buffers(_on_cuda(b), dev, 130, 256, 5)
+
+
+def test_calls_refuse_cpu_handles():
+    q = bq.alloc_outputs(Scheme("e4m3", "mx"), 4, 64, CPU, stats=False)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: bq.dequantize(q), lambda: bq.dequantize_rt(q), lambda: bq.qsnr(x, q), lambda: bq.gemm(q, q)):
+        with pytest.raises(ValueError):
+            call()
