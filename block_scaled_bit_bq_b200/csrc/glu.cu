@@ -32,6 +32,14 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
+// x cut to [-12, 12]; NaN stays NaN (fminf and fmaxf would give a bound).
+__device__ __forceinline__ float cut12(float x)
+{
+    float r;
+    asm("{\nmax.NaN.f32 %0, %1, 0fC1400000;\nmin.NaN.f32 %0, %0, 0f41400000;\n}" : "=f"(r) : "f"(x));
+    return r;
+}
+
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float GELU_2C = 1.5957691216057308f;                      // 2 sqrt(2 / pi)
 constexpr float GELU_K = 0.044715f;
@@ -47,7 +55,7 @@ __device__ __forceinline__ float logistic(float g, float& slope)
         if constexpr (SLOPE) slope = __fmaf_rn(__fmul_rn(g, s), __fadd_rn(1.0f, -s), s);
         return s;
     } else {
-        const float c = fminf(fmaxf(g, -12.0f), 12.0f), c2 = __fmul_rn(c, c);
+        const float c = cut12(g), c2 = __fmul_rn(c, c);
         const float v = __fmul_rn(c, __fmaf_rn(GELU_2C * GELU_K, c2, GELU_2C));
         const float s = rcp_approx(__fadd_rn(1.0f, ex2_approx(__fmul_rn(v, -LOG2E))));
         if constexpr (SLOPE) {

@@ -438,8 +438,10 @@ bq_status bq_linear_grad_weight(const void* dy, int32_t dy_dtype, int64_t lddy,
  * aligned; out: bf16 [rows, cols] contiguous, 32-byte aligned; codes uint8 [rows, cols],
  * 32-byte aligned; scales uint8 [rows, cols / 32], 4-byte aligned. cols % 32 == 0;
  * rows >= 0 (0: nothing is done); rows * cols <= 2^36 - 2048. Outputs may not overlap the
- * inputs or each other (dgate == dup: BQ_ERR_INVALID_ARG). NaN or Inf in g or u give
- * unspecified results in their own 32-element block. No workspace; enqueued on stream.
+ * inputs or each other (dgate == dup: BQ_ERR_INVALID_ARG). NaN in g or u gives NaN in h, and
+ * with FP8 copies (which hold NaN) in dg and, of g, in du; apart from these elements NaN or Inf
+ * in g or u give unspecified results in their own 32-element block. No workspace; enqueued on
+ * stream.
  */
 enum { BQ_ACT_SILU = 0, BQ_ACT_GELU_TANH = 1 };
 
