@@ -426,9 +426,11 @@ bq_status bq_linear_grad_weight(const void* dy, int32_t dy_dtype, int64_t lddy,
  *   bq_glu_backward:  du = dh a(G),  dg = dh U a'(G)   (G, U the dequantized copies)
  *
  * a(g) = g s(v), s the logistic function: v = g for BQ_ACT_SILU, v = 2 sqrt(2 / pi)
- * (g + 0.044715 g^3) for BQ_ACT_GELU_TANH (the tanh form of GELU). Arithmetic in fp32
- * (exp2 and reciprocal approximations of about 2^-22 relative error), each result rounded
- * once to bf16. The forward pass uses g and u as given, not their copies.
+ * (g + 0.044715 g^3) for BQ_ACT_GELU_TANH (the tanh form of GELU). Arithmetic in fp32, each
+ * result rounded once to bf16. s is good to a relative (8 + |v|) 2^-22 down to 2^-126 (v about
+ * -87.3: g = -87.3 under SiLU, -9.9 under GELU) and 0 below, so that h, du and dg may also be
+ * off by 2^-126 |g u|, 2^-126 |dh g| and 2^-126 |dh u| (1 + |g v'|); they are finite where the
+ * true values are. The forward pass uses g and u as given, not their copies.
  *
  * scheme: BQ_MX_BLOCK with BQ_FP8_E4M3, BQ_FP8_E5M2 or BQ_INT8_SYM, BQ_LAYOUT_ROWS,
  * hadamard = 0 (else BQ_ERR_UNSUPPORTED). bq_glu with scheme == NULL computes h alone (for
