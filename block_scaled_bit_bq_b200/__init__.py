@@ -107,6 +107,8 @@ def _lib() -> ctypes.CDLL:
         L.bq_glu_backward.argtypes = [vp, i64, i32, vp, vp, vp, vp, sp, i64, i64, i32, vp, i64, vp, i64, vp]
         L.bq_debug_skip_tile_copy.restype = ctypes.c_int
         L.bq_debug_skip_tile_copy.argtypes = [i32]
+        L.bq_debug_skip_linear_copy.restype = ctypes.c_int
+        L.bq_debug_skip_linear_copy.argtypes = [i32]
         L.bq_wait_timeouts.restype = ctypes.c_int
         L.bq_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
         rtp = ctypes.POINTER(BqRowTransform)
@@ -286,6 +288,13 @@ def bq_debug_skip_tile_copy(warp: int) -> None:
     _check(_lib().bq_debug_skip_tile_copy(int(warp)), "bq_debug_skip_tile_copy")
 
 
+def bq_debug_skip_linear_copy(cta: int) -> None:
+    """Test hook: in the next product of the linear layer on the tensor cores, CTA `cta` issues no
+    copies for its first stage, so that its waits run out (bounded) and bq_wait_timeouts counts
+    them."""
+    _check(_lib().bq_debug_skip_linear_copy(int(cta)), "bq_debug_skip_linear_copy")
+
+
 def bq_dequantize(codes: torch.Tensor, scales: torch.Tensor, zero_points: torch.Tensor | None,
                   tensor_scale: torch.Tensor | None, rows: int, cols: int, scheme: Scheme,
                   out: torch.Tensor, stream=None) -> None:
@@ -343,7 +352,7 @@ def pack_sign_bits(signs, device=None) -> torch.Tensor:
 
 
 def bq_wait_timeouts(reset: bool = False) -> int:
-    """Tile waits of the quantize kernels that gave up on the current device (each
+    """Waits of the quantize, GEMM and linear kernels that gave up on the current device (each
     leaves its call's outputs incomplete); synchronizes with the device."""
     c = ctypes.c_uint32(0)
     _check(_lib().bq_wait_timeouts(ctypes.byref(c), 1 if reset else 0), "bq_wait_timeouts")

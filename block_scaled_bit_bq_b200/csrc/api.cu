@@ -420,6 +420,13 @@ bq_status bq_debug_skip_tile_copy(int32_t warp)
     return BQ_OK;
 }
 
+bq_status bq_debug_skip_linear_copy(int32_t cta)
+{
+    if (cta < 0) return BQ_ERR_INVALID_ARG;
+    bq::linear_skip_copy((uint32_t)cta);
+    return BQ_OK;
+}
+
 bq_status bq_quantize_batch(const void* x, int32_t x_dtype, int64_t batch, int64_t rows, int64_t cols,
                             const bq_scheme* scheme, void* codes, void* scales, void* zero_points,
                             bq_stats* stats, void* workspace, size_t workspace_bytes, void* stream)

@@ -175,6 +175,8 @@ struct LinearArgs {
 cudaError_t launch_linear(int op, int fmt, bool nv, const LinearArgs& a, cudaStream_t st);
 // Waits of the linear kernels that gave up (each leaves that call's output incomplete). Synchronous.
 cudaError_t linear_wait_timeouts(unsigned int* count, bool reset);
+// The next launch of the tensor-core kernel skips that CTA's first copies of X (tests).
+void linear_skip_copy(uint32_t cta);
 
 // The gated activation (glu.cu). Forward: x0 = gate, x1 = up, y0 = h, codes and scales written
 // (null: none). Backward: x0 = dh, codes and scales read, y0 = dgate, y1 = dup.

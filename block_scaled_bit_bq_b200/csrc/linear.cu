@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 namespace bq {
 
@@ -313,6 +314,7 @@ struct MmaPlan {
     uint32_t blocks;        // of the contraction: 256 steps, four parts, each
     uint32_t split;         // CTAs per tile (a cluster): 1, 2, 4 or 8
     uint32_t pair;          // 1: tiles of 256 x 256 on pairs of CTAs (bt 128 each)
+    uint32_t skip_cta;      // fault injection for tests: this CTA issues no copies of X for its first stage
 };
 
 // Instruction descriptor of the bf16 MMA: fp32 accumulator (bits 4-5), bf16 operands (7-9,
@@ -431,6 +433,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
 {
     using W = Widen<FMT, NV>;
     constexpr uint32_t CP = Fmt<FMT>::four ? 4u : 2u;     // parts of a chunk of codes
+    constexpr std::integral_constant<int, ACQ_CTA> acq_cta{};
+    constexpr std::integral_constant<int, PAIR ? ACQ_SHARED : ACQ_CTA> acq_stage{};     // a stage is full
+    constexpr std::integral_constant<int, PAIR ? ACQ_CLUSTER : ACQ_CTA> acq_acc{};      // an accumulator is full, empty
     extern __shared__ uint8_t linear_smem[];
     __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], code_full[MAX_CHUNKS],
         code_empty[MAX_CHUNKS], acc_full[2], acc_empty[2], done_bar;
@@ -457,6 +462,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
     // parts past the contraction's end fill up its last block: they take part in every hand-over,
     // but nothing is copied, widened or multiplied for them
     auto live = [&](uint32_t part) { return (uint64_t)part * 64u < a.nc; };
+    // A warp's wait, and whether some warp has given up: the same answer for all lanes, since what
+    // follows (barriers of whole warps, tcgen05) wants them together
+    auto get = [](auto acq, uint64_t& bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait_ring<decltype(acq)::value>(smem_addr(&bar), parity)) != 0;
+    };
+    auto stopped = [&]() { return __any_sync(0xFFFFFFFFu, abort_flag) != 0; };
     // first i of a tile for this CTA, and first j of the tile
     auto tile_i0 = [&](uint32_t t) { return t % pl.tiles_i * (PAIR ? 256u : 128u) + (PAIR ? rank * 128u : 0u); };
     auto tile_j0 = [&](uint32_t t) { return t / pl.tiles_i * tile_j; };
@@ -506,11 +517,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         // ---- X tiles ----
         const bool leader = elect_one();
         uint32_t s = 0, round = 0;                   // slot of the ring, and how often it wrapped
-        for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+        bool go = true;
+        for (uint32_t t = first; t < pl.tiles && go; t += step) {
             const int j0 = (int)(tile_j0(t) + (PAIR ? rank * bt : 0u));
             for (uint32_t kk = 0; kk < tile_stages; ++kk) {
-                if (round > 0 && !mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u)) { abort_flag = 1; break; }
-                if (abort_flag) break;
+                go = (round == 0 || get(acq_cta, empty[s], (round - 1) & 1u)) && !stopped();
+                if (!go) break;
                 if (leader) {
                     const uint32_t fb = smem_addr(&full[s]);
                     uint32_t dst = base + s * stage_bytes + A_BYTES, part = p0 + kk * subs;
@@ -521,7 +533,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                     // cannot fall behind by a use of a slot, which a wait by parity would not tell
                     if (PAIR && rank != 0) mbar_arrive(fb);
                     else mbar_arrive_expect_tx(fb, (PAIR ? 2u : 1u) * n_live * b_bytes);
-                    for (uint32_t u = 0; u < n_live; ++u, ++part, dst += sub_bytes) {
+                    const bool skip = blockIdx.x == pl.skip_cta && t == first && kk == 0;     // tests only
+                    for (uint32_t u = 0; u < n_live && !skip; ++u, ++part, dst += sub_bytes) {
                         const int c = (int)(part * 64u);
                         if (OP == LIN_GRAD_WEIGHT) {
                             for (uint32_t x = 0; x < bt / 64u; ++x)
@@ -535,14 +548,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 if (++s == NS) { s = 0; ++round; }
             }
         }
-        // the copies in flight (at most one stage a slot) land before the CTA can exit: after an
-        // abort the full barriers may stay short of the widening warps' arrivals, so the wait
-        // (bounded) is for their time only (in a pair the first CTA waits for both: neither
-        // leaves before the other)
-        if (abort_flag) {
-            for (uint32_t j = 0; j < NS && (round > 0 || j < s); ++j)
-                (void)mbar_wait(smem_addr(&full[j]), (j < s ? round : round - 1) & 1u);
-        }
+        if (!go) abort_flag = 1;
     } else if (warp == 1) {
         // ---- MMAs: 16 steps are 32 bytes along a K-major row, 16 rows (2 KB) of an MN-major
         // chunk. The whole warp runs the loop, so that descriptors stay in uniform registers ----
@@ -552,12 +558,13 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         const uint64_t ad0 = OP == LIN_FORWARD ? operand_desc(base) : mn_desc(base);
         const uint64_t bd0 = OP == LIN_GRAD_WEIGHT ? mn_desc(base + A_BYTES) : operand_desc(base + A_BYTES);
         uint32_t s = 0, par = 0, i = 0, stage = 0;
+        bool go = true;
         if (PAIR && rank != 0) {
             // the second CTA of a pair only says when its codes of a stage are widened
-            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+            for (uint32_t t = first; t < pl.tiles && go; t += step) {
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
-                    if (!mbar_wait_ring(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
-                    if (abort_flag) break;
+                    go = get(acq_cta, full[s], par) && !stopped();
+                    if (!go) break;
                     if (leader) {
                         mbar_arrive_first_shared(smem_addr(&full[s]));
                         stages_done = ++stage;
@@ -567,14 +574,16 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 }
             }
         } else {
-            for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step, ++i) {
+            for (uint32_t t = first; t < pl.tiles && go; t += step, ++i) {
                 const uint32_t b = i & 1u;
-                if (i >= 2 && !mbar_wait_ring<PAIR ? ACQ_CLUSTER : ACQ_CTA>(smem_addr(&acc_empty[b]), (i / 2 - 1) & 1u)) { abort_flag = 1; break; }
+                go = (i < 2 || get(acq_acc, acc_empty[b], (i / 2 - 1) & 1u)) && !stopped();
+                if (!go) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + b * ACC_COLS;
                 uint32_t acc = 0;
                 for (uint32_t kk = 0; kk < tile_stages; ++kk) {
-                    if (!mbar_wait_ring<PAIR ? ACQ_SHARED : ACQ_CTA>(smem_addr(&full[s]), par)) { abort_flag = 1; break; }
+                    go = get(acq_stage, full[s], par);
+                    if (!go) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     for (uint32_t u = 0; u < subs; ++u) {
                         const uint64_t so = (s * stage_bytes + u * sub_bytes) >> 4, ad = ad0 + so, bd = bd0 + so;
@@ -592,7 +601,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                     __syncwarp();
                     if (++s == NS) { s = 0; par ^= 1u; }
                 }
-                if (abort_flag) break;
+                if (!go) break;
                 if (leader) tc_commit_all<PAIR>(smem_addr(&acc_full[b]));
                 __syncwarp();
             }
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
             if (leader) tc_commit_all<PAIR>(smem_addr(&done_bar));
             __syncwarp();
         }
-        if (!mbar_wait(smem_addr(&done_bar), 0u)) abort_flag = 1;
+        if (!mbar_wait(smem_addr(&done_bar), 0u) || !go) abort_flag = 1;
     } else if (warp < 2 + WIDEN_WARPS) {
         // ---- Q tiles: a thread takes 64 codes of one stored row: forward, row r of the tile and
         // the part's columns; gradients, row r of the part and half h of the tile's columns.
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 if (lane == 0) mbar_arrive(smem_addr(&code_empty[c]));
                 fetch(sc[1]);
                 if (ok && round > 0) ok = mbar_wait_ring(smem_addr(&empty[s]), (round - 1) & 1u);
-                ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
+                ok = __all_sync(0xFFFFFFFFu, ok && !abort_flag) != 0;
                 if (!ok) { abort_flag = 1; break; }
                 if (live(p0 + pk)) {
                     const uint32_t dst = base + s * stage_bytes + dst_off;
@@ -701,11 +710,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         // boxes of 256 (128) rows of the contraction x the tile's 128 columns ----
         const bool leader = elect_one();
         uint32_t c = 0, round = 0;
-        for (uint32_t t = first; t < pl.tiles && !abort_flag; t += step) {
+        bool go = true;
+        for (uint32_t t = first; t < pl.tiles && go; t += step) {
             const uint32_t i0 = tile_i0(t);
             for (uint32_t n = 0; n < tile_chunks; ++n) {
-                if (round > 0 && !mbar_wait_ring(smem_addr(&code_empty[c]), (round - 1) & 1u)) { abort_flag = 1; break; }
-                if (abort_flag) break;
+                go = (round == 0 || get(acq_cta, code_empty[c], (round - 1) & 1u)) && !stopped();
+                if (!go) break;
                 if (leader) {
                     const uint32_t part = p0 + n * CP, fb = smem_addr(&code_full[c]);
                     mbar_arrive_expect_tx(fb, CHUNK_BYTES);
@@ -716,11 +726,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
                 if (++c == pl.chunks) { c = 0; ++round; }
             }
         }
-        if (abort_flag) {
-            // let the copies in flight land before the CTA can exit (bounded)
-            for (uint32_t j = 0; j < pl.chunks && (round > 0 || j < c); ++j)
-                (void)mbar_wait(smem_addr(&code_full[j]), (j < c ? round : round - 1) & 1u);
-        }
+        if (!go) abort_flag = 1;
     } else {
         // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, i.e. 32 i, and
         // every second 32 columns ----
@@ -732,11 +738,11 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
             // a tile's whole contraction may lie before this: the wait goes on as long as stages do
             bool ok = false;
             for (uint32_t seen = stages_done, now;; seen = now) {
-                ok = mbar_wait_ring<PAIR ? ACQ_CLUSTER : ACQ_CTA>(smem_addr(&acc_full[b]), (n / 2) & 1u);
+                ok = mbar_wait_ring<acq_acc.value>(smem_addr(&acc_full[b]), (n / 2) & 1u);
                 now = stages_done;
                 if (ok || abort_flag || now == seen) break;
             }
-            ok = __all_sync(0xFFFFFFFFu, ok) && !abort_flag;
+            ok = __all_sync(0xFFFFFFFFu, ok && !abort_flag) != 0;
             if (!ok) { abort_flag = 1; break; }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t i0 = tile_i0(t) + q * 32u, j0 = tile_j0(t);
@@ -763,6 +769,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) k_linear_mma(const __grid_cons
         }
     }
     __syncwarp();
+    __syncthreads();                                 // no warp issues anything any more
+    // Every copy that was waited for has landed. A CTA that gave up may have issued others: it
+    // keeps its shared memory for another second
+    if (abort_flag) linger();
     if (PAIR) cluster_sync();                        // neither CTA leaves while the other's MMAs or arrivals may use it
     if (!PAIR && pl.split > 1) {
         cluster_sync();
@@ -830,6 +840,10 @@ cudaError_t x_map(const LinearArgs& a, uint32_t box_rows, CUtensorMap* map)
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Test hook (bq_debug_skip_linear_copy), consumed by the next launch.
+constexpr uint32_t NO_CTA = 0xFFFFFFFFu;
+std::atomic<uint32_t> g_skip_cta{NO_CTA};
+
 uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
 
 uint32_t plan_stage_bytes(const MmaPlan& p) { return p.subs * (A_BYTES + p.bt * 128u); }
@@ -869,6 +883,7 @@ MmaPlan make_mma_plan(int op, const LinearArgs& a, uint32_t sms)
     // codes are most of what is read, and their ring keeps the memory busy
     const uint32_t room = SMEM_ROOM, stage = plan_stage_bytes(p);
     p.stages = std::min(4u, (room - 2u * CHUNK_BYTES) / stage);          // four parts or more
+    p.skip_cta = g_skip_cta.exchange(NO_CTA, std::memory_order_acq_rel);
     p.chunks = std::min<uint32_t>(MAX_CHUNKS, (room - p.stages * stage) / CHUNK_BYTES) & ~1u;
     return p;
 }
@@ -954,6 +969,8 @@ cudaError_t launch_linear(int op, int fmt, bool nv, const LinearArgs& a, cudaStr
     if (fmt == BQ_INT8_SYM) return run_mma<LIN_GRAD_WEIGHT, BQ_INT8_SYM, false>(a, st);
     return cudaErrorInvalidValue;
 }
+
+void linear_skip_copy(uint32_t cta) { g_skip_cta.store(cta, std::memory_order_release); }
 
 cudaError_t linear_wait_timeouts(unsigned int* count, bool reset)
 {

@@ -156,6 +156,13 @@ __device__ __forceinline__ bool mbar_wait_ring(uint32_t bar, uint32_t parity)
     return ok;
 }
 
+// About WAIT_LIMIT_NS, for copies in flight that nothing waits for any more to land.
+__device__ __forceinline__ void linger()
+{
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < WAIT_LIMIT_NS) __nanosleep(100000);
+}
+
 // 16-byte shared-memory accesses.
 __device__ __forceinline__ void lds_v4(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3)
 {

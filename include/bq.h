@@ -399,8 +399,8 @@ bq_status bq_gemm(const void* a_codes, const void* a_scales, const float* a_tens
  * m == 0 (n == 0): an output without elements is left alone, and a gradient that sums over
  * no tokens (no outputs) is set to zero. Codes: 32-byte aligned; scales and the tensor scale
  * 4-byte aligned (BQ_ERR_ALIGNMENT). Non-finite x or dy, and NaN or Inf
- * codes of an FP8 X, follow IEEE arithmetic. No workspace; enqueued on stream; every wait in the kernels is bounded (bq_wait_timeouts counts those that
- * gave up).
+ * codes of an FP8 X, follow IEEE arithmetic. No workspace; enqueued on stream; every wait in
+ * the kernels is bounded (bq_wait_timeouts counts those that gave up).
  */
 bq_status bq_linear(const void* x, int32_t x_dtype, int64_t ldx,
                     const void* w_codes, const void* w_scales, const float* w_tensor_scale,
@@ -458,11 +458,13 @@ bq_status bq_glu_backward(const void* dh, int64_t ld_dh, int32_t dtype,
                           void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup, void* stream);
 
 /*
- * Bounded waits. The quantize kernels stage their input tiles in shared memory with
- * tensor-map bulk copies and wait for each on an mbarrier; a wait that has not
- * completed after about one second gives up instead of hanging. The kernel then stops
- * early and the call's outputs are incomplete. This is a failure of the device or
- * driver, not of the arguments.
+ * Bounded waits. The quantize kernels, bq_gemm and the linear layer's products stage their
+ * inputs in shared memory with tensor-map bulk copies and wait for each on an mbarrier; a
+ * wait that has not completed after about one second (in the linear layer's products, for a
+ * finished sum: after a second without progress) gives up instead of hanging. The kernel
+ * then stops early and the call's outputs are incomplete; it returns within a few seconds,
+ * with nothing left in flight. This is a failure of the device or driver, or of a device
+ * that other work holds for so long, not of the arguments.
  *
  * bq_wait_timeouts writes to *count how many such waits gave up on the current device
  * since the library was loaded or last reset (reset != 0 sets the count back to zero).
@@ -485,6 +487,17 @@ bq_status bq_wait_timeouts(uint32_t* count, int32_t reset);
  * consumes it resets it. warp < 0: BQ_ERR_INVALID_ARG.
  */
 bq_status bq_debug_skip_tile_copy(int32_t warp);
+
+/*
+ * The same for the linear layer's products on the tensor cores (bq_linear of more than 16
+ * tokens, bq_linear_grad_input, bq_linear_grad_weight): in the next such call, CTA number
+ * `cta` issues no copies of the bf16 operand for its first stage. The wait for it gives up,
+ * the CTA (of a pair of CTAs that share a tile: both) stops, waits a second for its other
+ * copies and ends; the tiles that it had are not written (of a tile whose sum several CTAs
+ * share: are of no value) and bq_wait_timeouts counts one more for each CTA that stopped.
+ * One-shot, also where the call has fewer CTAs. cta < 0: BQ_ERR_INVALID_ARG.
+ */
+bq_status bq_debug_skip_linear_copy(int32_t cta);
 
 /* QSNR = -10 log10(err2 / x2) in dB from a host copy of the stats ("INT vs FP at fine
  * granularity" §4.1): +inf when err2 = 0, NaN when x2 = 0 with err2 > 0 or for a NULL
