@@ -144,6 +144,10 @@ class Scheme:
         blk = self.block or {"mx": 32, "nv": 16, "tile2d": 128}.get(self.gran, 0)
         return Scheme(self.fmt, self.gran, blk, sd, bool(self.hadamard), self.layout)
 
+    def __getstate__(self):
+        """The fields alone: what calls keep on the scheme (see _c_scheme) is not saved with it."""
+        return {n: getattr(self, n) for n in self.__dataclass_fields__}
+
     def c(self) -> BqScheme:
         s = self.resolved()
         return BqScheme(FORMATS[s.fmt], GRANULARITIES[s.gran], s.block, DT[s.scale_dtype], int(s.hadamard),

@@ -1,7 +1,10 @@
 """Handles (Quantized) whose buffers do not hold what their scheme and shape say are refused
 before any launch (no GPU)."""
 
+import copy
 import dataclasses
+import io
+import pickle
 
 import pytest
 import torch
@@ -94,3 +97,18 @@ def test_calls_refuse_cpu_handles():
     for call in (lambda: bq.dequantize(q), lambda: bq.dequantize_rt(q), lambda: bq.qsnr(x, q), lambda: bq.gemm(q, q)):
         with pytest.raises(ValueError):
             call()
+
+
+# a handle that has been through a call is saved and loaded as before it
+def test_saved_handles_hold_no_cached_forms():
+    q = _handle(SCHEMES[1], 4, 64)
+    for s in (q.scheme, SCHEMES[1]):
+        bq._c_scheme(s)
+        bq._resolved(s)
+    assert set(pickle.loads(pickle.dumps(q.scheme)).__dict__) == {f.name for f in dataclasses.fields(Scheme)}
+    f = io.BytesIO()
+    torch.save(q, f)
+    f.seek(0)
+    with torch.serialization.safe_globals([bq.Quantized, bq.Scheme]):
+        r = torch.load(f, weights_only=True)
+    assert r.scheme == q.scheme and torch.equal(r.codes, q.codes) and copy.deepcopy(q).scheme == q.scheme
