@@ -552,6 +552,13 @@ def qsnr(x: torch.Tensor, q: Quantized, workspace: torch.Tensor | None = None, s
 
 # ---------------------------------------------------------------------------
 # A linear layer over block-scaled data, and the gated activation between two of them
+#
+# Plain functions: results carry no autograd graph, whatever their inputs do. Rows of bf16 inputs
+# may be apart; an input whose rows are not a multiple of 8 elements apart (16 in the gated
+# activation), whose columns are not adjacent or whose start is not aligned to as many elements
+# is copied first (2 bytes an element read and written once more). A contiguous [m, n] with n
+# % 8 != 0 is one: a caller with an odd number of outputs who keeps dy in rows of a multiple of 8
+# (a slice of a wider buffer) saves the copy on each call.
 # ---------------------------------------------------------------------------
 
 _OUT_DT = {torch.bfloat16: 0, torch.float32: 2}
@@ -648,7 +655,8 @@ def _out(out: torch.Tensor | None, rows: int, cols: int, dtype, dev: torch.devic
 def linear(x: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
     """x W^T: bf16 x [m, k] (rows may be apart) and a 4-bit weight w (E2M1 under "mx" or "nv")
-    of [n, k] -> [m, n] of dtype (or of out's)."""
+    of [n, k] -> [m, n] of dtype (or of out's). No autograd: linear_grad_input and
+    linear_grad_weight are its gradients."""
     dev = w.codes.device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -665,7 +673,8 @@ def linear(x: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tenso
 
 def linear_grad_input(dy: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
-    """dy W: the gradient of linear's x, from bf16 dy [m, n] and the weight [n, k] -> [m, k]."""
+    """dy W: the gradient of linear's x, from bf16 dy [m, n] and the weight [n, k] -> [m, k]. A
+    dy whose rows are not a multiple of 8 elements apart is copied first."""
     dev = w.codes.device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -683,7 +692,8 @@ def linear_grad_input(dy: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out:
 def linear_grad_weight(dy: torch.Tensor, x: Quantized, dtype=torch.float32, out: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
     """dy^T X: the gradient of linear's weight, from bf16 dy [m, n] and the layer's input kept
-    in 8 bits (E4M3, E5M2 or INT8 under "mx") x of [m, k] -> [n, k]."""
+    in 8 bits (E4M3, E5M2 or INT8 under "mx") x of [m, k] -> [n, k]. A dy whose rows are not a
+    multiple of 8 elements apart is copied first."""
     dev = x.codes.device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
