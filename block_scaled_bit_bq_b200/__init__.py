@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -428,17 +429,26 @@ def alloc_outputs(scheme: Scheme, rows: int, cols: int, device, stats: bool = Tr
     return Quantized(s, rows, cols, codes, scales, zps, ts, st)
 
 
+# the bytes of a scheme's codes, scales, zero points and tensor scale for a shape (plain values)
+_sizes = functools.lru_cache(maxsize=1024)(bq_buffer_sizes)
+
+
 def _buffers(q, dev: torch.device, rows: int, cols: int, batch: int = 1) -> None:
     """Refuses a handle (Quantized, QuantizedBatch) whose buffers do not hold batch tensors of
     [rows, cols] under its scheme: another device, not contiguous, or too short."""
     if dev.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
-    sizes = bq_buffer_sizes(q.scheme, rows, cols)
-    for name, need in zip(("codes", "scales", "zero_points", "tensor_scale"), sizes):
-        t = getattr(q, name, None)
-        if need and t is not None and (t.device != dev or not t.is_contiguous()
-                                       or t.numel() * t.element_size() < need * batch):
-            raise ValueError(f"{name}: expected {need * batch} contiguous bytes on {dev}")
+    cb, sb, zb, tb = _sizes(q.scheme, rows, cols)
+    c, s = q.codes, q.scales
+    if c.device != dev or not c.is_contiguous() or c.nbytes < cb * batch:
+        raise ValueError(f"codes: expected {cb * batch} contiguous bytes on {dev}")
+    if s.device != dev or not s.is_contiguous() or s.nbytes < sb * batch:
+        raise ValueError(f"scales: expected {sb * batch} contiguous bytes on {dev}")
+    if zb or tb:
+        for name, need in (("zero_points", zb * batch), ("tensor_scale", tb)):
+            t = getattr(q, name, None) if need else None
+            if t is not None and (t.device != dev or not t.is_contiguous() or t.nbytes < need):
+                raise ValueError(f"{name}: expected {need} contiguous bytes on {dev}")
 
 
 @dataclass
@@ -564,11 +574,12 @@ def qsnr(x: torch.Tensor, q: Quantized, workspace: torch.Tensor | None = None, s
 _OUT_DT = {torch.bfloat16: 0, torch.float32: 2}
 
 
-def _c_scheme(scheme: Scheme) -> BqScheme:
-    """scheme.c(), kept on the scheme (a frozen value), for the calls whose host time counts."""
+def _c_scheme(scheme: Scheme):
+    """A reference to scheme.c() as the C entry points take it, kept on the scheme (a frozen
+    value), for the calls whose host time counts."""
     c = scheme.__dict__.get("_c")
     if c is None:
-        c = scheme.c()
+        c = ctypes.byref(scheme.c())
         object.__setattr__(scheme, "_c", c)
     return c
 
@@ -581,7 +592,7 @@ def _raw_stream(dev: torch.device) -> int:
 def _elsewhere(dev: torch.device, stream) -> bool:
     if dev.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
-    return stream is not None or dev.index != torch.cuda.current_device()
+    return stream is not None or dev.index != torch._C._cuda_getDevice()     # (current_device() without its checks)
 
 
 @contextlib.contextmanager
@@ -628,18 +639,20 @@ def _handle(q: Quantized, dev: torch.device) -> None:
     read or write past their end: on another device, not contiguous, or shorter than its scheme
     and shape ask. (Other schemes are refused by the calls that this serves.)"""
     s, rows, cols = q.scheme, q.rows, q.cols
-    if s.gran not in ("mx", "nv"):
+    nv = s.gran == "nv"
+    if not nv and s.gran != "mx":
         return
-    nb = cols // (32 if s.gran == "mx" else 16)
-    codes, scales, ts = q.codes, q.scales, q.tensor_scale
+    codes, scales = q.codes, q.scales
     if (codes.device != dev or not codes.is_contiguous() or codes.element_size() != 1
             or codes.numel() < (rows * cols // 2 if s.fmt in FOUR_BIT else rows * cols)):
         raise ValueError(f"the codes are not contiguous bytes of a {s.fmt} [{rows}, {cols}] tensor on {dev}")
     if (scales.device != dev or not scales.is_contiguous() or scales.element_size() != 1
-            or scales.numel() < ((rows + 127) // 128 * 128 if s.layout == "gemm" else rows) * nb):
-        raise ValueError(f"the scales are not contiguous bytes of [{rows}, {nb}] blocks on {dev}")
-    if s.gran == "nv" and ts is not None and (ts.device != dev or ts.dtype is not torch.float32 or ts.numel() < 1):
-        raise ValueError(f"the tensor scale is not fp32 on {dev}")
+            or scales.numel() < ((rows + 127) // 128 * 128 if s.layout == "gemm" else rows) * (cols // (16 if nv else 32))):
+        raise ValueError(f"the scales are not contiguous bytes of [{rows}, {cols // (16 if nv else 32)}] blocks on {dev}")
+    if nv:
+        ts = q.tensor_scale
+        if ts is not None and (ts.device != dev or ts.dtype is not torch.float32 or ts.numel() < 1):
+            raise ValueError(f"the tensor scale is not fp32 on {dev}")
 
 
 def _out(out: torch.Tensor | None, rows: int, cols: int, dtype, dev: torch.device) -> torch.Tensor:
@@ -666,7 +679,7 @@ def linear(x: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out: torch.Tenso
     m, n = x.shape[0], w.rows
     y = _out(out, m, n, dtype, dev)
     _check(_lib().bq_linear(x.data_ptr(), 0, ld, w.codes.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale), m, n,
-                            w.cols, ctypes.byref(_c_scheme(w.scheme)), y.data_ptr(), _OUT_DT[y.dtype],
+                            w.cols, _c_scheme(w.scheme), y.data_ptr(), _OUT_DT[y.dtype],
                             _raw_stream(dev)), "bq_linear")
     return y
 
@@ -684,7 +697,7 @@ def linear_grad_input(dy: torch.Tensor, w: Quantized, dtype=torch.bfloat16, out:
     m, k = dy.shape[0], w.cols
     dx = _out(out, m, k, dtype, dev)
     _check(_lib().bq_linear_grad_input(dy.data_ptr(), 0, ld, w.codes.data_ptr(), w.scales.data_ptr(),
-                                       _ptr(w.tensor_scale), m, w.rows, k, ctypes.byref(_c_scheme(w.scheme)),
+                                       _ptr(w.tensor_scale), m, w.rows, k, _c_scheme(w.scheme),
                                        dx.data_ptr(), _OUT_DT[dx.dtype], _raw_stream(dev)), "bq_linear_grad_input")
     return dx
 
@@ -703,7 +716,7 @@ def linear_grad_weight(dy: torch.Tensor, x: Quantized, dtype=torch.float32, out:
     n, k = dy.shape[1], x.cols
     dw = _out(out, n, k, dtype, dev)
     _check(_lib().bq_linear_grad_weight(dy.data_ptr(), 0, ld, x.codes.data_ptr(), x.scales.data_ptr(), x.rows, n, k,
-                                        ctypes.byref(_c_scheme(x.scheme)), dw.data_ptr(), _OUT_DT[dw.dtype],
+                                        _c_scheme(x.scheme), dw.data_ptr(), _OUT_DT[dw.dtype],
                                         _raw_stream(dev)), "bq_linear_grad_weight")
     return dw
 
@@ -761,14 +774,14 @@ def glu(gate: torch.Tensor, up: torch.Tensor, scheme: Scheme | None = None, act:
         g, u = _glu_copy(s, rows, cols, dev), _glu_copy(s, rows, cols, dev)
         ckpt = GluCheckpoint(g, u, act)
     else:
-        s, g, u = scheme.resolved(), ckpt.gate, ckpt.up
+        s, g, u = _resolved(scheme), ckpt.gate, ckpt.up
         if g.scheme != s or u.scheme != s or (g.rows, g.cols) != (rows, cols) or (u.rows, u.cols) != (rows, cols):
             raise ValueError("the checkpoint's buffers are of another scheme or shape")
         _handle(g, dev)
         _handle(u, dev)
         ckpt.act = act
     _check(_lib().bq_glu(gate.data_ptr(), ldg, up.data_ptr(), ldu, 0, rows, cols, a, h.data_ptr(),
-                         ctypes.byref(_c_scheme(s)), g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(),
+                         _c_scheme(s), g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(),
                          u.scales.data_ptr(), _raw_stream(dev)), "bq_glu")
     return h, ckpt
 
@@ -782,7 +795,7 @@ def glu_backward(dh: torch.Tensor, ckpt: GluCheckpoint, out=None, stream=None):
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return glu_backward(dh, ckpt, out)
-    if (u.rows, u.cols) != (rows, cols) or u.scheme != g.scheme:
+    if u.rows != rows or u.cols != cols or (u.scheme is not g.scheme and u.scheme != g.scheme):
         raise ValueError("the two copies must be of one shape and scheme")
     _handle(g, dev)
     _handle(u, dev)
@@ -797,6 +810,6 @@ def glu_backward(dh: torch.Tensor, ckpt: GluCheckpoint, out=None, stream=None):
         if tg is not dg or tu is not du:
             raise ValueError("out must have unit column stride, rows a multiple of 16 elements apart and be 32-byte aligned")
     _check(_lib().bq_glu_backward(dh.data_ptr(), ldh, 0, g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(),
-                                  u.scales.data_ptr(), ctypes.byref(_c_scheme(g.scheme)), rows, cols, ACTS[ckpt.act],
+                                  u.scales.data_ptr(), _c_scheme(g.scheme), rows, cols, ACTS[ckpt.act],
                                   dg.data_ptr(), ldg, du.data_ptr(), ldu, _raw_stream(dev)), "bq_glu_backward")
     return dg, du
