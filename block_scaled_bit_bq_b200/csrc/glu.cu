@@ -149,16 +149,44 @@ __device__ __forceinline__ void chunk_floats(const uint32_t (&w)[4], uint32_t sc
     dequant_chunk<FMT, SK_UE8M0>(us, raw, v);
 }
 
-// d u t, p = d u. Where p overflows (t may be as small as 2^-126, or 0) the slope goes first: u t
-// is a normal number then (|u| >= 1, |t| < 1.14), and the result finite where d u t is.
-__device__ __forceinline__ float times_slope(float d, float u, float p, float t)
+// dg of a chunk once more, for products dh u that overflow: the slope may bring them back (it may be
+// as small as 2^-126, or 0) and goes first there: u a' is a normal number then (|u| >= 1, |a'| <
+// 1.14), and dg finite where the true value is. Four elements at a time, which keeps its registers
+// below the pass's own.
+template <int FMT, int ACT>
+__device__ __forceinline__ void dgate_again(const GluArgs& a, uint32_t c, uint32_t row, uint32_t col)
 {
-    return fabsf(p) <= 3.402823466e38f ? __fmul_rn(p, t) : __fmul_rn(d, __fmul_rn(u, t));
+    constexpr float largest = 3.402823466e38f;
+    const uint32_t gs = __ldg(a.scales0 + (c >> 1)), us = __ldg(a.scales1 + (c >> 1));
+#pragma unroll 1
+    for (uint32_t q = 0; q < 4; ++q) {
+        const uint2 dw = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.x0) + row * a.ldx0 + col) + q);
+        const uint32_t gw[4] = {__ldg(reinterpret_cast<const uint32_t*>(a.codes0) + (size_t)c * 4u + q), 0u, 0u, 0u};
+        const uint32_t uw[4] = {__ldg(reinterpret_cast<const uint32_t*>(a.codes1) + (size_t)c * 4u + q), 0u, 0u, 0u};
+        float2 g[8], u[8];
+        chunk_floats<FMT>(gw, gs, g);
+        chunk_floats<FMT>(uw, us, u);
+        uint32_t r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w = i ? dw.y : dw.x;
+            const float2 d = make_float2(bf_lo(w), bf_hi(w)), p = mul2(d, u[i]);
+            float t0, t1;
+            (void)logistic<ACT, true>(g[i].x, t0);
+            (void)logistic<ACT, true>(g[i].y, t1);
+            r[i] = bf16_pair(fabsf(p.x) <= largest ? __fmul_rn(p.x, t0) : __fmul_rn(d.x, __fmul_rn(u[i].x, t0)),
+                             fabsf(p.y) <= largest ? __fmul_rn(p.y, t1) : __fmul_rn(d.y, __fmul_rn(u[i].y, t1)));
+        }
+        st_v2(reinterpret_cast<__nv_bfloat16*>(a.y0) + row * a.ldy0 + col + 4u * q, r);
+    }
 }
 
-// (five CTAs an SM: at 50 registers, four, INT8 under GELU took 59 us instead of 55 at 4096 x 11008)
+// The look for such a product (the largest |dh u| of a chunk) shows under GELU, whose arithmetic is
+// next to HBM's time (8192 x 4096 E5M2: 42.5 -> 43.3 us); chosen for each element it took 43.7, and
+// SiLU's passes 1.3 % more. INT8 takes 54-56 registers by itself, four CTAs an SM: five are 4 %
+// faster at 4096 x 11008 under GELU (57.8 -> 55.8 us).
 template <int FMT, int ACT>
-__global__ void __launch_bounds__(GLU_THREADS, 5) k_glu_backward(const GluArgs a)
+__global__ void __launch_bounds__(GLU_THREADS, FMT == BQ_INT8_SYM ? 5 : 0) k_glu_backward(const GluArgs a)
 {
     pdl_wait();
     const uint64_t c64 = (uint64_t)blockIdx.x * GLU_THREADS + threadIdx.x;
@@ -174,19 +202,21 @@ __global__ void __launch_bounds__(GLU_THREADS, 5) k_glu_backward(const GluArgs a
         chunk_floats<FMT>(gc, gs, g);
         chunk_floats<FMT>(uc, us, u);
         uint32_t dg[8], du[8];
+        float most = 0.0f;                           // of |dh u|
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float t0, t1;
             const float s0 = logistic<ACT, true>(g[i].x, t0), s1 = logistic<ACT, true>(g[i].y, t1);
             const float2 d = make_float2(bf_lo(dh[i]), bf_hi(dh[i]));
             const float2 ru = mul2(d, mul2(g[i], make_float2(s0, s1)));
-            const float2 p = mul2(d, u[i]);
-            const float2 rg = make_float2(times_slope(d.x, u[i].x, p.x, t0), times_slope(d.y, u[i].y, p.y, t1));
+            const float2 p = mul2(d, u[i]), rg = mul2(p, make_float2(t0, t1));
             du[i] = bf16_pair(ru.x, ru.y);
             dg[i] = bf16_pair(rg.x, rg.y);
+            most = fmaxf(most, fmaxf(fabsf(p.x), fabsf(p.y)));
         }
         st_v8(reinterpret_cast<__nv_bfloat16*>(a.y0) + row * a.ldy0 + col, dg);
         st_v8(reinterpret_cast<__nv_bfloat16*>(a.y1) + row * a.ldy1 + col, du);
+        if (most > 3.402823466e38f) dgate_again<FMT, ACT>(a, c, row, col);
     }
 }
 
