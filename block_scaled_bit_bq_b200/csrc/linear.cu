@@ -286,10 +286,13 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, R * MT == 1 ? 3 : 2) k_linear
 // than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction and adds up its parts
 // through distributed shared memory, in rank order: no workspace, and the same sums every time.
 // Waits give up after a second as in the block-scaled GEMM (counted in g_linear_wait_timeouts), the
-// epilogue's for an accumulator after a second in which no stage was done.
+// epilogue's for an accumulator after a second in which no stage was done. A pair's stage is whole
+// on the first CTA's barrier: both CTAs' copies complete there, and the second CTA's codes are handed
+// over there. tests/linear_ring_model.py is a model of all this.
 //
-// 4096 tokens x 11008 x 4096: 272 us forward, 269 input gradient, 301 weight gradient (1.36,
-// 1.37 and 1.23 PFLOP/s; tensor pipe active 61-74 %, the widening warps' ALU 45-50 %). With few
+// 4096 tokens x 11008 x 4096: 270 us forward (NV), 289-340 input gradient (MX), 303-330 weight
+// gradient (E4M3), as the power cap's clock has it (1.1-1.37 PFLOP/s; tensor pipe active 61-74 %,
+// the widening warps' ALU 45-49 %); dequantizing to bf16 and a library product take 248-284. With few
 // tokens the hand-over of a part (about 0.35 us whatever the tile's width) bounds it.
 // ---------------------------------------------------------------------------
 
