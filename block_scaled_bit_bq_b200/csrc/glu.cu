@@ -184,7 +184,7 @@ __device__ __forceinline__ void dgate_again(const GluArgs& a, uint32_t c, uint32
 // The look for such a product (the largest |dh u| of a chunk) shows under GELU, whose arithmetic is
 // next to HBM's time (8192 x 4096 E5M2: 42.5 -> 43.3 us); chosen for each element it took 43.7, and
 // SiLU's passes 1.3 % more. INT8 takes 54-56 registers by itself, four CTAs an SM: five are 4 %
-// faster at 4096 x 11008 under GELU (57.8 -> 55.8 us).
+// faster at 4096 x 11008 under GELU (57.8 -> 56.2 us).
 template <int FMT, int ACT>
 __global__ void __launch_bounds__(GLU_THREADS, FMT == BQ_INT8_SYM ? 5 : 0) k_glu_backward(const GluArgs a)
 {
@@ -214,9 +214,10 @@ __global__ void __launch_bounds__(GLU_THREADS, FMT == BQ_INT8_SYM ? 5 : 0) k_glu
             dg[i] = bf16_pair(rg.x, rg.y);
             most = fmaxf(most, fmaxf(fabsf(p.x), fabsf(p.y)));
         }
-        st_v8(reinterpret_cast<__nv_bfloat16*>(a.y0) + row * a.ldy0 + col, dg);
-        st_v8(reinterpret_cast<__nv_bfloat16*>(a.y1) + row * a.ldy1 + col, du);
+        // (dh is read again before anything is written)
         if (most > 3.402823466e38f) dgate_again<FMT, ACT>(a, c, row, col);
+        else st_v8(reinterpret_cast<__nv_bfloat16*>(a.y0) + row * a.ldy0 + col, dg);
+        st_v8(reinterpret_cast<__nv_bfloat16*>(a.y1) + row * a.ldy1 + col, du);
     }
 }
 
